@@ -23,6 +23,9 @@ __all__ = [
     "attn_prefill_qk8", "prefill_qk8", "attn_quantize_i8", "quantize_i8", "attn_prefill_qki8",
     "prefill_qki8", "attn_prefill_poly", "prefill_poly", "attn_decode", "attn_decode_ex",
     "attn_decode_noalloc", "attn_decode_rule", "attn_decode_paged", "decode_paged", "RULE_GROUP", "RULE_PER_HEAD", "RULE_SINK_SEED",
+    "attn_qk_norm_rope", "qk_norm_rope", "attn_cache_write_e4m3", "cache_write_e4m3",
+    "attn_cache_read_e4m3", "cache_read_e4m3", "attn_tree_paged", "tree_paged", "attn_tree_paged_e4m3",
+    "tree_paged_e4m3", "attn_tree_workspace_bytes",
     "attn_decode_split_len", "attn_decode_tile", "attn_decode_workspace_bytes",
     "attn_set_stream", "attn_sync_status", "attn_last_timeout_site", "attn_set_wait_limit_ms",
     "attn_test_withhold_copy", "attn_status_string", "attn_shutdown", "prefill", "decode", "STATUS",
@@ -52,6 +55,7 @@ def lib() -> ctypes.CDLL:
         raise AttnError(-1, f"loading {LIB_PATH} (not built; run python -m block_skipping_softmax_b200.build)")
     L = ctypes.CDLL(LIB_PATH)
     vp, ci, cf, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    ll = ctypes.c_longlong
     sig = {
         "attn_prefill": (ci, [vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, ci, ci]),
         "attn_prefill_ex": (ci, [vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, ci, ci, vp, vp]),
@@ -68,6 +72,12 @@ def lib() -> ctypes.CDLL:
         "attn_decode_rule": (ci, [vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, ci, vp, vp, vp, sz]),
         "attn_decode_paged": (ci, [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, cf, ci, vp, vp,
                                    vp, sz]),
+        "attn_qk_norm_rope": (ci, [vp] * 8 + [ci] * 7 + [cf, vp, ll, vp]),
+        "attn_cache_write_e4m3": (ci, [vp] * 7 + [ci] * 5 + [vp, vp]),
+        "attn_cache_read_e4m3": (ci, [vp] * 7 + [ci] * 5 + [vp, vp]),
+        "attn_tree_paged": (ci, [vp] * 8 + [ci] * 9 + [vp, vp, sz]),
+        "attn_tree_paged_e4m3": (ci, [vp] * 10 + [ci] * 9 + [vp, vp, sz]),
+        "attn_tree_workspace_bytes": (sz, [ci] * 7),
         "attn_decode_split_len": (ci, [ci, ci, ci]),
         "attn_decode_tile": (ci, []),
         "attn_decode_workspace_bytes": (sz, [ci, ci, ci, ci, ci]),
@@ -165,6 +175,50 @@ def attn_decode_paged(q, K_pages, V_pages, block_table, seq_lens, o, B, Hq, Hkv,
 def attn_decode_noalloc(q, K, V, o, B, Hq, Hkv, L, d, tau, stream=None, skip_mask=None) -> int:
     """Decode with the library's fixed scratch array: no device allocation."""
     return lib().attn_decode_noalloc(q, K, V, o, B, Hq, Hkv, L, d, float(tau), stream, skip_mask)
+
+
+def _strides(values):
+    return (ctypes.c_longlong * len(values))(*values)
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, B, N, Hq, Hkv, d, rot_dim,
+                      interleaved, eps, strides, pos_stride_b, stream=None) -> int:
+    """``strides``: 12 ints (batch, token and head stride of q, k, q_out, k_out, in elements)."""
+    return lib().attn_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, B, N, Hq, Hkv, d,
+                                   rot_dim, int(interleaved), eps, _strides(strides), pos_stride_b, stream)
+
+
+def attn_cache_write_e4m3(k, v, slots, K_codes, V_codes, K_scales, V_scales, B, N, Hkv, num_pages, d, strides,
+                          stream=None) -> int:
+    """``strides``: 6 ints (batch, token and head stride of k and v, in elements)."""
+    return lib().attn_cache_write_e4m3(k, v, slots, K_codes, V_codes, K_scales, V_scales, B, N, Hkv, num_pages,
+                                       d, _strides(strides), stream)
+
+
+def attn_cache_read_e4m3(K_codes, V_codes, K_scales, V_scales, slots, k, v, B, N, Hkv, num_pages, d, strides,
+                         stream=None) -> int:
+    """``strides``: 6 ints (batch, token and head stride of k and v, in elements)."""
+    return lib().attn_cache_read_e4m3(K_codes, V_codes, K_scales, V_scales, slots, k, v, B, N, Hkv, num_pages,
+                                      d, _strides(strides), stream)
+
+
+def attn_tree_paged(q, K_pages, V_pages, block_table, seq_lens, cu_q, tree_mask, o, B, max_q, total_q, Hq, Hkv,
+                    num_pages, max_pages_per_seq, max_seq_len, d, stream=None, ws=None, ws_bytes=0) -> int:
+    return lib().attn_tree_paged(q, K_pages, V_pages, block_table, seq_lens, cu_q, tree_mask, o, B, max_q,
+                                 total_q, Hq, Hkv, num_pages, max_pages_per_seq, max_seq_len, d, stream, ws,
+                                 ws_bytes)
+
+
+def attn_tree_paged_e4m3(q, K_codes, V_codes, K_scales, V_scales, block_table, seq_lens, cu_q, tree_mask, o, B,
+                         max_q, total_q, Hq, Hkv, num_pages, max_pages_per_seq, max_seq_len, d, stream=None,
+                         ws=None, ws_bytes=0) -> int:
+    return lib().attn_tree_paged_e4m3(q, K_codes, V_codes, K_scales, V_scales, block_table, seq_lens, cu_q,
+                                      tree_mask, o, B, max_q, total_q, Hq, Hkv, num_pages, max_pages_per_seq,
+                                      max_seq_len, d, stream, ws, ws_bytes)
+
+
+def attn_tree_workspace_bytes(B, max_q, total_q, Hq, Hkv, max_seq_len, d) -> int:
+    return lib().attn_tree_workspace_bytes(B, max_q, total_q, Hq, Hkv, max_seq_len, d)
 
 
 def attn_decode_split_len(B, Hkv, L) -> int:
@@ -446,3 +500,266 @@ def decode_paged(q, K_pages, V_pages, block_table, seq_lens, max_seq_len: int, t
                            mask.data_ptr() if mask is not None else None)
     _check(st, "attn_decode_paged")
     return (o, mask) if skip_mask else o
+
+
+# ---- cache and tree helpers ---------------------------------------------------
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise AttnError(1, what)
+
+
+def _on_current_device(what: str, *tensors):
+    """Every tensor is on the current CUDA device (the library launches there)."""
+    import torch
+
+    for t in tensors:
+        _need(t is None or t.is_cuda, f"{what} (tensors must be CUDA tensors)")
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        _need(t is None or t.device.index == dev, f"{what} (tensors must be on the current CUDA device)")
+
+
+class _Launch:
+    """The stream of one call.  Memory that the call allocates belongs to that
+    stream; tensors that meet it from another one are recorded on it, so that
+    the caching allocator keeps them until the call's kernels are done."""
+
+    def __init__(self, stream, *tensors):
+        import torch
+
+        self.current = torch.cuda.current_stream()
+        self.stream = self.current if stream is None else stream
+        self.other = self.stream.cuda_stream != self.current.cuda_stream
+        if self.other:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+    def empty(self, shape, dtype, device):
+        import torch
+
+        if not self.other:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(self.current)
+        return t
+
+
+def _token_layout(x):
+    """(B, N, H, d, strides) of [tokens, H, d] or [B, H, N, d] with contiguous d;
+    strides of axes of length 1 count as 0."""
+    if x.dim() == 3:
+        (N, H, d), (sn, sh, sd) = x.shape, x.stride()
+        B, sb = 1, 0
+    else:
+        (B, H, N, d), (sb, sh, sn, sd) = x.shape, x.stride()
+    _need(sd == 1, "tensors need contiguous heads")
+    return B, N, H, d, (sb if B > 1 else 0, sn if N > 1 else 0, sh if H > 1 else 0)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, out=None, stream=None):
+    """Norms of queries and keys for each head, and their rotation by position, in one pass.
+
+    q, k: bf16 CUDA tensors [tokens, H, d] or [B, H, N, d], of any strides that
+    are multiples of 8 (d contiguous), for instance slices of a fused
+    projection.  positions: int32 [tokens], or [N] or [B, N].  inv_freq:
+    float32 [rot_dim / 2], None for no rotation.  q_weight, k_weight: bf16 [d],
+    None for no norm.  interleaved: the pairs are (2i, 2i+1) instead of
+    (i, i + rot_dim/2).  Returns (q, k), contiguous, or ``out`` = (q, k), which
+    may be the inputs themselves.
+    """
+    import torch
+
+    what = "qk_norm_rope"
+    _need(q.dim() in (3, 4) and k.dim() == q.dim(), f"{what} (q and k must be [tokens, H, d] or [B, H, N, d])")
+    B, N, Hq, d, sq = _token_layout(q)
+    Bk, Nk, Hkv, dk, sk = _token_layout(k)
+    _need((B, N, d) == (Bk, Nk, dk), f"{what} (q and k must have the same tokens and head size)")
+    _need(q.dtype == torch.bfloat16 and k.dtype == torch.bfloat16, f"{what} (q and k must be bf16)")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    pos_stride = 0
+    if rot:
+        _need(inv_freq.dtype == torch.float32 and inv_freq.is_contiguous(), f"{what} (inv_freq must be float32)")
+        shapes = ((N,), (B, N)) if q.dim() == 4 else ((N,),)
+        _need(positions.dtype == torch.int32 and positions.shape in shapes and
+              (N == 1 or positions.stride(-1) == 1), f"{what} (positions must be int32 [N] or [B, N])")
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    for w in (q_weight, k_weight):
+        _need(w is None or (w.dtype == torch.bfloat16 and w.shape == (d,) and (w.is_contiguous())),
+              f"{what} (weights must be bf16 [d])")
+    _on_current_device(what, q, k, q_weight, k_weight, *((positions, inv_freq) if rot else ()))
+    run = _Launch(stream, q, k, positions, inv_freq, q_weight, k_weight, *(out or ()))
+    if out is None:
+        qo, ko = (run.empty(x.shape, x.dtype, x.device) for x in (q, k))
+    else:
+        qo, ko = out
+        for x, y in ((q, qo), (k, ko)):
+            _need(y.shape == x.shape and y.dtype == torch.bfloat16, f"{what} (out must be bf16 of the inputs' shapes)")
+        _on_current_device(what, qo, ko)
+    so, sp = _token_layout(qo)[4], _token_layout(ko)[4]
+    st = attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(),
+                           positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None,
+                           None if q_weight is None else q_weight.data_ptr(),
+                           None if k_weight is None else k_weight.data_ptr(), B, N, Hq, Hkv, d, rot, interleaved,
+                           eps, sq + sk + so + sp, pos_stride, run.stream.cuda_stream)
+    _check(st, "attn_qk_norm_rope")
+    return qo, ko
+
+
+def _check_codes(what, K_codes, V_codes, K_scales, V_scales):
+    import torch
+
+    _need(K_codes.dim() == 4 and K_codes.shape[2] == attn_decode_tile(),
+          f"{what} (codes must be [num_pages, Hkv, 64, d])")
+    for c in (K_codes, V_codes):
+        _need(c.dtype == torch.uint8 and c.shape == K_codes.shape and c.is_contiguous(),
+              f"{what} (codes must be contiguous uint8 of one shape)")
+    for s in (K_scales, V_scales):
+        _need(s.dtype == torch.float32 and s.shape == K_codes.shape[:3] and s.is_contiguous(),
+              f"{what} (scales must be contiguous float32 [num_pages, Hkv, 64])")
+
+
+def _check_slots(what, slots, B, N, packed):
+    import torch
+
+    shape = (N,) if packed else (B, N)
+    _need(slots.dtype == torch.int64 and slots.shape == shape and slots.is_contiguous(),
+          f"{what} (slots must be contiguous int64, one for each token)")
+
+
+def cache_write_e4m3(k, v, slots, K_codes, V_codes, K_scales, V_scales, stream=None) -> None:
+    """Quantise keys and values to e4m3 and write them into a paged cache, in place.
+
+    k, v: bf16 CUDA tensors [tokens, Hkv, d] or [B, Hkv, N, d] (strides as in
+    qk_norm_rope).  slots: int64 [tokens] or [B, N]: page * 64 + key, no two
+    alike; a token whose slot lies outside the pool (-1) is not written.
+    K_codes, V_codes: uint8 [num_pages, Hkv, 64, d]; K_scales, V_scales: float32
+    [num_pages, Hkv, 64].
+    """
+    import torch
+
+    what = "cache_write_e4m3"
+    _need(k.dim() in (3, 4) and k.shape == v.shape, f"{what} (k and v must be [tokens, H, d] or [B, H, N, d])")
+    _need(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16, f"{what} (k and v must be bf16)")
+    B, N, Hkv, d, sk = _token_layout(k)
+    sv = _token_layout(v)[4]
+    _check_codes(what, K_codes, V_codes, K_scales, V_scales)
+    _need(K_codes.shape[1] == Hkv and K_codes.shape[3] == d, f"{what} (the pool has other heads than k)")
+    _check_slots(what, slots, B, N, k.dim() == 3)
+    every = (k, v, slots, K_codes, V_codes, K_scales, V_scales)
+    _on_current_device(what, *every)
+    run = _Launch(stream, *every)
+    st = attn_cache_write_e4m3(k.data_ptr(), v.data_ptr(), slots.data_ptr(), K_codes.data_ptr(),
+                               V_codes.data_ptr(), K_scales.data_ptr(), V_scales.data_ptr(), B, N, Hkv,
+                               K_codes.shape[0], d, sk + sv, run.stream.cuda_stream)
+    _check(st, "attn_cache_write_e4m3")
+
+
+def cache_read_e4m3(K_codes, V_codes, K_scales, V_scales, slots, out=None, stream=None):
+    """(k, v) of the given slots of an e4m3 cache, as bf16.
+
+    slots int64 [tokens] gives [tokens, Hkv, d]; [B, N] gives [B, Hkv, N, d].  A
+    slot outside the pool reads zeros.  ``out`` = (k, v) writes into existing
+    tensors of those shapes (strides as in qk_norm_rope).
+    """
+    import torch
+
+    what = "cache_read_e4m3"
+    _check_codes(what, K_codes, V_codes, K_scales, V_scales)
+    pages, Hkv, _, d = K_codes.shape
+    _need(slots.dim() in (1, 2), f"{what} (slots must be [tokens] or [B, N])")
+    shape = (slots.shape[0], Hkv, d) if slots.dim() == 1 else (slots.shape[0], Hkv, slots.shape[1], d)
+    every = (K_codes, V_codes, K_scales, V_scales, slots)
+    _on_current_device(what, *every)
+    run = _Launch(stream, *every, *(out or ()))
+    if out is None:
+        k, v = (run.empty(shape, torch.bfloat16, slots.device) for _ in range(2))
+    else:
+        k, v = out
+        for t in (k, v):
+            _need(t.shape == shape and t.dtype == torch.bfloat16, f"{what} (out must be bf16 of shape {shape})")
+        _on_current_device(what, k, v)
+    B, N, _, _, sk = _token_layout(k)
+    sv = _token_layout(v)[4]
+    _check_slots(what, slots, B, N, slots.dim() == 1)
+    st = attn_cache_read_e4m3(K_codes.data_ptr(), V_codes.data_ptr(), K_scales.data_ptr(), V_scales.data_ptr(),
+                              slots.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, Hkv, pages, d, sk + sv,
+                              run.stream.cuda_stream)
+    _check(st, "attn_cache_read_e4m3")
+    return k, v
+
+
+def tree_paged(q, K_pages, V_pages, block_table, seq_lens, cu_q, max_q: int, max_seq_len: int, tree_mask=None,
+               out=None, stream=None, workspace=None):
+    """Attention of each sequence's drafted tokens over its paged bf16 cache.
+
+    q: bf16 [total_q, Hq, d], sequence b's tokens at rows cu_q[b]..cu_q[b+1]
+    (cu_q int32 [B + 1], at most max_q <= 64 tokens each).  K_pages, V_pages,
+    block_table and seq_lens as in decode_paged; seq_lens count the drafted
+    tokens' own keys, which are each sequence's last.  tree_mask: int64
+    [total_q], bit j set iff the token sees drafted key j; None: a chain.
+    Rows of no sequence stay as they are in ``out``, and are undefined without
+    it.  ``workspace``: optional uint8 CUDA tensor of at least
+    attn_tree_workspace_bytes(...) bytes.
+    """
+    import torch
+
+    for t in (K_pages, V_pages):
+        _need(t.dtype == torch.bfloat16 and t.is_contiguous() and t.shape == K_pages.shape,
+              "tree_paged (pages must be contiguous bf16 of one shape)")
+    return _tree("tree_paged", q, K_pages, V_pages, None, None, block_table, seq_lens, cu_q, max_q, max_seq_len,
+                 tree_mask, out, stream, workspace)
+
+
+def tree_paged_e4m3(q, K_codes, V_codes, K_scales, V_scales, block_table, seq_lens, cu_q, max_q: int,
+                    max_seq_len: int, tree_mask=None, out=None, stream=None, workspace=None):
+    """tree_paged over the e4m3 cache that cache_write_e4m3 writes."""
+    _check_codes("tree_paged_e4m3", K_codes, V_codes, K_scales, V_scales)
+    return _tree("tree_paged_e4m3", q, K_codes, V_codes, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
+                 max_seq_len, tree_mask, out, stream, workspace)
+
+
+def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q, max_seq_len, tree_mask, out,
+          stream, workspace):
+    import torch
+
+    _need(q.dim() == 3 and q.dtype == torch.bfloat16 and q.is_contiguous(),
+          f"{what} (q must be contiguous bf16 [total_q, Hq, d])")
+    total, Hq, d = q.shape
+    _need(K.dim() == 4 and K.shape[2] == attn_decode_tile() and K.shape[3] == d,
+          f"{what} (the cache must be [num_pages, Hkv, 64, d])")
+    pages, Hkv = K.shape[0], K.shape[1]
+    for t in (block_table, seq_lens, cu_q):
+        _need(t.dtype == torch.int32 and t.is_contiguous(),
+              f"{what} (block_table, seq_lens and cu_q must be contiguous int32)")
+    B = seq_lens.numel()
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and cu_q.numel() == B + 1,
+          f"{what} (block_table must be [B, max_pages] and cu_q [B + 1])")
+    if tree_mask is not None:
+        _need(tree_mask.dtype == torch.int64 and tree_mask.shape == (total,) and tree_mask.is_contiguous(),
+              f"{what} (tree_mask must be contiguous int64 [total_q])")
+    every = (q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, tree_mask, out, workspace)
+    _on_current_device(what, *every)
+    run = _Launch(stream, *every)
+    o = run.empty(q.shape, q.dtype, q.device) if out is None else out
+    if out is not None:
+        _need(o.shape == q.shape and o.dtype == torch.bfloat16 and o.is_contiguous(),
+              f"{what} (out must be contiguous bf16 of q's shape)")
+    ws = workspace
+    if ws is None:
+        need = attn_tree_workspace_bytes(B, max_q, total, Hq, Hkv, max_seq_len, d)
+        ws = run.empty((need,), torch.uint8, q.device) if need else None
+    mask = None if tree_mask is None else tree_mask.data_ptr()
+    ws_ptr, ws_bytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    tail = (block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), mask, o.data_ptr(), B, max_q, total, Hq,
+            Hkv, pages, block_table.shape[1], max_seq_len, d, run.stream.cuda_stream, ws_ptr, ws_bytes)
+    if K_scales is None:
+        st = attn_tree_paged(q.data_ptr(), K.data_ptr(), V.data_ptr(), *tail)
+    else:
+        st = attn_tree_paged_e4m3(q.data_ptr(), K.data_ptr(), V.data_ptr(), K_scales.data_ptr(),
+                                  V_scales.data_ptr(), *tail)
+    _check(st, "attn_" + what)
+    return o

@@ -1,0 +1,240 @@
+// Writing a paged KV cache as e4m3 codes, and reading it back as bf16.
+//
+// A key vector x of one head (d elements) is quantised by itself, as it is
+// written: s = 2^k, k the smallest integer >= -126 with max|x| <= 448 * 2^k, and
+// code = e4m3(x / s), rounded to nearest, ties to even.  That is the rule of
+// attn_quantize_e4m3 with the vector as the group: a longer group would have
+// to be quantised again whenever a later key is larger.  With s a power of two
+// x / s and code * s are exact, so reading back is exact in bf16, and the
+// attention over the codes is attention over the values read back.
+//
+// Both directions are bound by HBM (a token's heads: 4 d bytes of bf16 and
+// 2 (d + 4) of codes and scales).  A vector is held by D/8 lanes, 16 bytes of
+// bf16 and 8 of codes each, so its maximum is a 3- or 4-step butterfly and
+// every access a full 128-byte line or two for each vector; a group of lanes
+// takes up to four vectors, all loaded before the first is reduced.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace bss {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPage = kDecodeTile;  // keys of a page
+constexpr unsigned kFull = 0xffffffffu;
+
+struct CacheArgs {
+  const void* x[2];  // k, v (bf16; written by the read)
+  uint8_t* codes[2];
+  float* scales[2];
+  const long long* slots;
+  long long xs[2][3];  // strides in elements: batch, token, head
+  long long rows;      // B * N * 2 * Hkv
+  long long n_slots;   // num_pages * 64
+  int N, Hkv;
+};
+
+// Row = one head's key or value vector of one token; the 2 Hkv rows of a token
+// are neighbours, keys first.
+struct Row {
+  bool valid;
+  int side, h;
+  long long x_at;     // element offset in x[side]
+  long long slot;     // -1 where the token has none
+  long long code_at;  // vector index in codes[side] / scales[side]
+};
+
+__device__ __forceinline__ Row row_of(const CacheArgs& a, long long r) {
+  Row w;
+  w.valid = r < a.rows;
+  const unsigned per = 2u * a.Hkv;
+  const unsigned t = w.valid ? static_cast<unsigned>(r / per) : 0u;  // token: B * N < 2^31
+  const unsigned hh = w.valid ? static_cast<unsigned>(r - static_cast<long long>(t) * per) : 0u;
+  w.side = hh >= static_cast<unsigned>(a.Hkv);
+  w.h = hh - (w.side ? a.Hkv : 0);
+  const unsigned b = t / a.N, n = t % a.N;
+  w.x_at = w.side ? b * a.xs[1][0] + n * a.xs[1][1] + w.h * a.xs[1][2]
+                  : b * a.xs[0][0] + n * a.xs[0][1] + w.h * a.xs[0][2];
+  w.slot = w.valid ? a.slots[t] : -1;
+  if (w.slot < 0 || w.slot >= a.n_slots) w.slot = -1;
+  w.code_at = w.slot < 0 ? 0 : ((w.slot / kPage) * a.Hkv + w.h) * kPage + w.slot % kPage;
+  return w;
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a) {
+  constexpr int kLanes = D / 8;
+  constexpr int kGroups = kThreads / kLanes;
+  const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  Row row[R];
+  uint4 u[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    row[r] = row_of(a, (static_cast<long long>(blockIdx.x) * R + r) * kGroups + group);
+    u[r] = make_uint4(0, 0, 0, 0);
+    if (row[r].slot >= 0)
+      u[r] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>((row[r].side ? a.x[1] : a.x[0])) +
+                                             row[r].x_at + c * 8);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t w[4] = {u[r].x, u[r].y, u[r].z, u[r].w};
+    uint32_t m = 0;  // max |x| as bits: non-negative floats order like their bits
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+    // m = f 2^e with f in [1, 2); 448 = 1.75 * 2^8.  max|x| <= 448 * 2^k holds
+    // first at k = e - 8 when f <= 1.75, else at e - 7.  A subnormal m (e field
+    // 0) lies below 448 * 2^-126, the least scale.  1/s is then exact too:
+    // |k| <= 126.
+    int k = static_cast<int>(m >> 23) - 127 - 8 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
+    k = max(k, -126);
+    float s = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+    float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    if (m == 0) s = inv = 1.f;
+    if (m >= 0x7f800000u) s = inv = __uint_as_float(0x7fc00000u);  // inf or NaN in the vector
+    uint32_t out[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint16_t lo, hi;  // cvt packs its first source into the upper byte
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(lo)
+          : "f"(__uint_as_float(w[2 * i] & 0xffff0000u) * inv),
+            "f"(__uint_as_float(w[2 * i] << 16) * inv));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(hi)
+          : "f"(__uint_as_float(w[2 * i + 1] & 0xffff0000u) * inv),
+            "f"(__uint_as_float(w[2 * i + 1] << 16) * inv));
+      out[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+    }
+    if (row[r].slot >= 0) {
+      *reinterpret_cast<uint2*>((row[r].side ? a.codes[1] : a.codes[0]) + row[r].code_at * D + c * 8) =
+          make_uint2(out[0], out[1]);
+      if (c == 0) (row[r].side ? a.scales[1] : a.scales[0])[row[r].code_at] = s;
+    }
+  }
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a) {
+  constexpr int kLanes = D / 8;
+  constexpr int kGroups = kThreads / kLanes;
+  const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  Row row[R];
+  uint2 u[R];
+  float s[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    row[r] = row_of(a, (static_cast<long long>(blockIdx.x) * R + r) * kGroups + group);
+    u[r] = make_uint2(0, 0);
+    s[r] = 0.f;
+    if (row[r].slot >= 0) {
+      u[r] = *reinterpret_cast<const uint2*>((row[r].side ? a.codes[1] : a.codes[0]) + row[r].code_at * D + c * 8);
+      s[r] = (row[r].side ? a.scales[1] : a.scales[0])[row[r].code_at];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t pair = (i & 1) ? (i < 2 ? u[r].x : u[r].y) >> 16 : (i < 2 ? u[r].x : u[r].y);
+      uint32_t h2;  // two halves: every e4m3 value is exact in fp16
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(pair)));
+      const __half2 h = *reinterpret_cast<const __half2*>(&h2);
+      out[i] = pack_bf16x2(__low2float(h) * s[r], __high2float(h) * s[r]);
+    }
+    if (row[r].valid)
+      *reinterpret_cast<uint4*>(
+          const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>((row[r].side ? a.x[1] : a.x[0]))) +
+          row[r].x_at + c * 8) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+template <int D, bool WRITE, int R>
+int launch_r(const CacheArgs& a, cudaStream_t s) {
+  constexpr int kGroups = kThreads / (D / 8);
+  const long long grid = (a.rows + kGroups * R - 1) / (kGroups * R);
+  if (grid > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if constexpr (WRITE)
+    cache_write_kernel<D, R><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
+  else
+    cache_read_kernel<D, R><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Vectors of a group: one where the launch fits the 148 SMs at once, else four.
+template <int D, bool WRITE>
+int launch_d(const CacheArgs& a, cudaStream_t s) {
+  constexpr int kGroups = kThreads / (D / 8);
+  if (a.rows <= 148LL * 4 * kGroups) return launch_r<D, WRITE, 1>(a, s);
+  return launch_r<D, WRITE, 4>(a, s);
+}
+
+int run(const void* k, const void* v, const int64_t* slots, const void* K_codes,
+        const void* V_codes, const float* K_scales, const float* V_scales, int B, int N, int Hkv,
+        int num_pages, int d, const long long* strides, void* stream, bool write) {
+  if (!k || !v || !slots || !K_codes || !V_codes || !K_scales || !V_scales || !strides)
+    return ATTN_ERR_INVALID_ARG;
+  if (!ptr_aligned(k, 16) || !ptr_aligned(v, 16) || !ptr_aligned(K_codes, 16) ||
+      !ptr_aligned(V_codes, 16) || !ptr_aligned(K_scales, 16) || !ptr_aligned(V_scales, 16) ||
+      !ptr_aligned(slots, 8))
+    return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || N <= 0 || Hkv <= 0 || num_pages <= 0 || (d != 64 && d != 128))
+    return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 6; ++i)
+    if (strides[i] % 8 != 0) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N > 0x7fffffffLL || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  int dev = 0;
+  int* status = nullptr;
+  const int st = device_context(&dev, &status);
+  if (st != ATTN_OK) return st;
+  CacheArgs a{};
+  a.x[0] = k;
+  a.x[1] = v;
+  a.codes[0] = static_cast<uint8_t*>(const_cast<void*>(K_codes));
+  a.codes[1] = static_cast<uint8_t*>(const_cast<void*>(V_codes));
+  a.scales[0] = const_cast<float*>(K_scales);
+  a.scales[1] = const_cast<float*>(V_scales);
+  a.slots = reinterpret_cast<const long long*>(slots);
+  for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < 3; ++i) a.xs[t][i] = strides[3 * t + i];
+  a.rows = static_cast<long long>(B) * N * 2 * Hkv;
+  a.n_slots = static_cast<long long>(num_pages) * kPage;
+  a.N = N;
+  a.Hkv = Hkv;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 64) return write ? launch_d<64, true>(a, s) : launch_d<64, false>(a, s);
+  return write ? launch_d<128, true>(a, s) : launch_d<128, false>(a, s);
+}
+
+}  // namespace
+
+}  // namespace bss
+
+extern "C" {
+
+int attn_cache_write_e4m3(const void* k, const void* v, const int64_t* slots, void* K_codes,
+                          void* V_codes, float* K_scales, float* V_scales, int B, int N, int Hkv,
+                          int num_pages, int d, const long long* strides, void* stream) {
+  return bss::run(k, v, slots, K_codes, V_codes, K_scales, V_scales, B, N, Hkv, num_pages, d,
+                  strides, stream, true);
+}
+
+int attn_cache_read_e4m3(const void* K_codes, const void* V_codes, const float* K_scales,
+                         const float* V_scales, const int64_t* slots, void* k, void* v, int B,
+                         int N, int Hkv, int num_pages, int d, const long long* strides,
+                         void* stream) {
+  return bss::run(k, v, slots, K_codes, V_codes, K_scales, V_scales, B, N, Hkv, num_pages, d,
+                  strides, stream, false);
+}
+
+}  // extern "C"

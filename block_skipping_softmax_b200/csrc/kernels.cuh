@@ -82,4 +82,42 @@ struct DecodeLaunch {
 
 int launch_decode(const DecodeLaunch& a);
 
+// Attention of the drafted tokens of each sequence over its paged cache.
+struct TreeLaunch {
+  const void* q;  // [total_q, Hq, d] bf16
+  const void* K;  // page pool [num_pages, Hkv, 64, d]: bf16, or e4m3 codes
+  const void* V;
+  const float* k_scales;  // e4m3: [num_pages, Hkv, 64]; null with a bf16 pool
+  const float* v_scales;
+  const int* block_table;  // [B, max_pages]
+  const int* seq_lens;     // [B]
+  const int* cu_q;         // [B + 1]
+  const unsigned long long* mask;  // [total_q], null: a chain
+  void* o;
+  int B, max_q, total_q, Hq, Hkv, num_pages, max_pages, L, d;
+  float scale_log2;
+  int split_len;  // keys per split, a multiple of kDecodeTile
+  int n_splits;
+  float* o_part;    // [total_q * Hq, n_splits, d] fp32, with n_splits > 1
+  float* lse_part;  // [total_q * Hq, n_splits]
+  int* status;
+  unsigned long long wait_limit_ns;
+  cudaStream_t stream;
+};
+
+int launch_tree(const TreeLaunch& a);
+
+// Tensor map over a pool of e4m3 codes [groups, 64, D], d fastest: boxes of a
+// whole group (64 keys), rows swizzled as 128 bytes (D = 128) or 64 (D = 64);
+// groups past the end read as zeros.
+bool tma_map_codes(CUtensorMap* m, const void* base, long long groups, int D);
+
+// Current device (sm_100 checked) and its device status word (api.cu).
+int device_context(int* dev, int** status);
+unsigned long long wait_limit_ns();
+
+inline bool ptr_aligned(const void* p, unsigned n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
 }  // namespace bss

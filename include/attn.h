@@ -311,6 +311,136 @@ ATTN_API int attn_decode_noalloc(const void* q, const void* K, const void* V, vo
                                  int Hq, int Hkv, int L, int d, float tau, void* stream,
                                  uint8_t* skip_mask);
 
+/*
+ * Norms of queries and keys for each head, with the rotation by position in
+ * the same pass: the step between the projection and attn_prefill,
+ * attn_decode or the cache.  For every token (b, n) and every head x of q
+ * [Hq, d] and of k [Hkv, d]:
+ *   y = x * rsqrt(mean(x^2) + eps) * w      (w null: y = x)
+ *   (y_a, y_b) <- (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
+ *   t = positions[b, n] * inv_freq[i]
+ * for the pairs i of the first rot_dim elements: (a, b) = (i, i + rot_dim/2),
+ * or (2i, 2i + 1) when interleaved is not 0.  fp32 throughout, the angle
+ * exact in fp64, one rounding to bf16 at the end.
+ *   q, k, q_out, k_out  bf16.  strides: 12 HOST values, in elements: batch,
+ *       token and head stride of q, k, q_out and k_out, in this order (the d
+ *       elements of a head are contiguous); multiples of 8.  So a slice of a
+ *       fused projection [tokens, Hq + 2 Hkv, d] goes in as it is, and
+ *       [B, H, N, d] comes out.  A packed batch [tokens, H, d] is B = 1.  An
+ *       output may be its input (same pointer and strides); other overlaps
+ *       are not allowed.
+ *   positions  device int32, token (b, n) at b * pos_stride_b + n; any value.
+ *   inv_freq   device float [rot_dim / 2].  Both may be null if rot_dim = 0.
+ *   q_weight, k_weight  bf16 [d], nullable (no norm on that side).
+ *   rot_dim    a multiple of 16, 0 <= rot_dim <= d.  d in {64, 128}.
+ *   Errors: ATTN_ERR_INVALID_ARG for null or unaligned pointers (16 bytes for
+ *   bf16 tensors), non-positive sizes, a stride or rot_dim that is not
+ *   allowed, eps negative, infinite or NaN; ATTN_ERR_UNSUPPORTED for B * N
+ *   from 2^31 or Hq + Hkv from 65536, and off sm_100; ATTN_ERR_CUDA.
+ */
+ATTN_API int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                               const int32_t* positions, const float* inv_freq,
+                               const void* q_weight, const void* k_weight, int B, int N, int Hq,
+                               int Hkv, int d, int rot_dim, int interleaved, float eps,
+                               const long long* strides, long long pos_stride_b, void* stream);
+
+/*
+ * Write keys and values into a paged cache of e4m3 codes.  Each vector (the d
+ * elements of one KV head of one token) gets its own scale s = 2^k, k the
+ * smallest integer >= -126 with max|x| <= 448 * 2^k (a zero vector 1, a vector
+ * holding inf or NaN NaN), and the codes e4m3(x / s), rounded to nearest, ties
+ * to even: attn_quantize_e4m3 with the vector as the group.
+ *   k, v    bf16, token (b, n), head h at strides in elements: 6 HOST values,
+ *           batch, token and head stride of k, then of v; multiples of 8.
+ *   slots   device int64 [B, N], contiguous: token (b, n) goes to page
+ *           slot / 64, key slot % 64.  A slot outside [0, 64 num_pages) (-1 for
+ *           a padded token) is not written.  The slots written must differ
+ *           from each other.
+ *   K_codes, V_codes    uint8 [num_pages, Hkv, 64, d], 16-byte aligned.
+ *   K_scales, V_scales  float [num_pages, Hkv, 64], 16-byte aligned.
+ *   Everything else in the pool stays as it is.  d in {64, 128}.
+ *   Errors: ATTN_ERR_INVALID_ARG for null or unaligned pointers, non-positive
+ *   sizes, another d, strides that are not multiples of 8;
+ *   ATTN_ERR_UNSUPPORTED for B * N from 2^31, Hkv from 65536, more than 2^31
+ *   blocks, and off sm_100; ATTN_ERR_CUDA.
+ */
+ATTN_API int attn_cache_write_e4m3(const void* k, const void* v, const int64_t* slots,
+                                   void* K_codes, void* V_codes, float* K_scales, float* V_scales,
+                                   int B, int N, int Hkv, int num_pages, int d,
+                                   const long long* strides, void* stream);
+
+/*
+ * Read slots of such a cache back: k and v get code * scale, which is exact in
+ * bf16 for what attn_cache_write_e4m3 wrote (but for |x| >= 248 * 2^120, whose
+ * code stands for 2^128: inf in bf16).  A slot outside the pool reads
+ * zeros.  Slots may repeat.  Other arguments and errors as
+ * attn_cache_write_e4m3, strides those of the outputs.
+ */
+ATTN_API int attn_cache_read_e4m3(const void* K_codes, const void* V_codes, const float* K_scales,
+                                  const float* V_scales, const int64_t* slots, void* k, void* v,
+                                  int B, int N, int Hkv, int num_pages, int d,
+                                  const long long* strides, void* stream);
+
+/*
+ * Attention of the drafted tokens of each sequence over its paged cache
+ * (speculative decoding: a tree of candidates is scored in one call).  Exact
+ * attention: no tile is skipped.
+ *   q, o       bf16 [total_q, Hq, d]: sequence b's tokens are rows cu_q[b] to
+ *              cu_q[b + 1] - 1 (as cu_seqlens of attn_prefill_varlen), of which
+ *              the first T_b = min(rows, max_q) count.  Rows of o that belong
+ *              to no counted token are not written.
+ *   K_pages, V_pages, block_table, max_pages_per_seq, max_seq_len
+ *              as attn_decode_paged; a page id outside the pool reads zeros.
+ *   seq_lens   device int32 [B]: keys of sequence b, the T_b drafted tokens'
+ *              own keys among them, which are the last T_b (token i's key is
+ *              key len_b - T_b + i; with len_b < T_b, key i).  Used as
+ *              min(len_b, max_seq_len); 0 is allowed.
+ *   tree_mask  device uint64 [total_q], 8-byte aligned: bit j of a token's
+ *              word is set iff it sees drafted key j (its ancestors and
+ *              itself).  Every token sees all keys before the drafted ones.
+ *              Null: a chain, token i sees drafted keys 0 to i; with one token
+ *              a sequence this is the decode of single tokens.
+ *   max_q      1 to 64.
+ *   A token that sees no key gets 0.  Slots past len_b may hold anything.  A
+ *   drafted key or value that is not finite reaches only the tokens that see
+ *   it, whose output is then NaN.
+ *   ws         device workspace of attn_tree_workspace_bytes(...) bytes, 256-byte
+ *              aligned; null where that is 0.  Its contents do not matter, and
+ *              are not used by a later call.  Calls that may overlap on the GPU
+ *              need one each.
+ *   Any Hq / Hkv.  d in {64, 128}.
+ *   Errors: ATTN_ERR_INVALID_ARG as attn_decode_paged, for max_q outside 1..64,
+ *   and for a workspace that is missing, unaligned or too small;
+ *   ATTN_ERR_UNSUPPORTED for B from 65536, (num_pages + 1) * Hkv from 2^31, or
+ *   Hkv * ceil(max_q * Hq / Hkv / 16) from 65536, and off sm_100; ATTN_ERR_CUDA.
+ */
+ATTN_API int attn_tree_paged(const void* q, const void* K_pages, const void* V_pages,
+                             const int32_t* block_table, const int32_t* seq_lens,
+                             const int32_t* cu_q, const uint64_t* tree_mask, void* o, int B,
+                             int max_q, int total_q, int Hq, int Hkv, int num_pages,
+                             int max_pages_per_seq, int max_seq_len, int d, void* stream, void* ws,
+                             size_t ws_bytes);
+
+/*
+ * attn_tree_paged over a cache of e4m3 codes as attn_cache_write_e4m3 writes
+ * it: key k of a page means K_codes * K_scales, value k V_codes * V_scales
+ * (powers of two; 16-byte aligned).  Exact attention over the values that
+ * attn_cache_read_e4m3 reads back; a key or value whose scale is NaN makes the
+ * tokens that see it NaN.
+ */
+ATTN_API int attn_tree_paged_e4m3(const void* q, const void* K_codes, const void* V_codes,
+                                  const float* K_scales, const float* V_scales,
+                                  const int32_t* block_table, const int32_t* seq_lens,
+                                  const int32_t* cu_q, const uint64_t* tree_mask, void* o, int B,
+                                  int max_q, int total_q, int Hq, int Hkv, int num_pages,
+                                  int max_pages_per_seq, int max_seq_len, int d, void* stream,
+                                  void* ws, size_t ws_bytes);
+
+/* Workspace bytes of attn_tree_paged and attn_tree_paged_e4m3: a function of
+ * these sizes only, 0 where none is needed and for invalid arguments. */
+ATTN_API size_t attn_tree_workspace_bytes(int B, int max_q, int total_q, int Hq, int Hkv,
+                                          int max_seq_len, int d);
+
 /* Split length in keys (a multiple of 64) used by decode: a deterministic
  * function of (B, Hkv, L) only.  Returns -1 for non-positive arguments. */
 ATTN_API int attn_decode_split_len(int B, int Hkv, int L);
