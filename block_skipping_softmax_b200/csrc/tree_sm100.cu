@@ -77,10 +77,19 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 __device__ __forceinline__ float lds_f32(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
   return v;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
 }
 
 // Two e4m3 codes in the upper bytes of the halfwords of w (the lower bytes may
@@ -89,9 +98,7 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
 // included.  Exact.  The NaN code (0x7f) comes out as 480: the writer never
 // stores it under a finite scale, and a NaN scale makes the value NaN.
 __device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t w) {
-  uint32_t x = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(0x7b807b80u));
-  return x;
+  return mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), 0x7b807b80u);
 }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -556,6 +563,528 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Kernel for many rows: 128 rows a CTA on tcgen05.
+//
+//   warp 0      copies: K and V pages, a ring in shared memory
+//   warp 1      TMEM, and the one thread that issues the MMAs:
+//                 S_j = Q K_j^T (two buffers), O += P_j V_j (P read from TMEM)
+//   warps 2-5   softmax: a thread owns the row of TMEM lane 32 (warp % 4) + lane
+//   warps 6...  tiles: e4m3 codes to bf16 (4 warps), or the check of the tiles
+//               that hold drafted keys (2 warps, bf16 pool)
+//
+// A tile is one page of 64 keys, so that TMEM holds O and two S in 256 columns
+// and two CTAs share an SM: one's softmax runs beside the other's MMAs.  The
+// rows past the last one are zero queries; softmax warps without a row leave.
+constexpr int kMmaRows = 128;
+
+template <int D, bool E4M3>
+struct BigCfg {
+  static constexpr int kPrep = E4M3 ? 4 : 2;  // warps that convert or check tiles
+  static constexpr int kThreads = (6 + kPrep) * 32;
+  static constexpr int kPanels = D / 64;
+  static constexpr int kQPanel = kMmaRows * 128;
+  static constexpr int kTile = kPage * D * 2;  // K or V of a page as bf16
+  static constexpr int kTilePanel = kPage * 128;
+  static constexpr int kRaw = kPage * D;       // as codes
+  static constexpr int kRing = E4M3 ? (D == 128 ? 5 : 8) : (D == 128 ? 4 : 6);  // tiles in flight
+  static constexpr int kSlot = E4M3 ? kRaw : kTile;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffConv = kOffQ + kMmaRows * D * 2;        // e4m3: bf16 K, bf16 V
+  static constexpr int kOffRing = kOffConv + (E4M3 ? 2 * kTile : 0);
+  static constexpr int kOffScale = kOffRing + kRing * kSlot;       // e4m3: [slot][64] floats
+  static constexpr int kOffBar = kOffScale + (E4M3 ? kRing * kPage * 4 : 0);
+  // full[ring], empty[ring], q_full, s_full[2], p_full[2], pv_done, o_final,
+  // checked[2]; bf16: drafted[2]; e4m3: ready[K, V], free[K, V]
+  static constexpr int kBars = 2 * kRing + 13;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;
+  static constexpr int kSmem = kOffMisc + 64 + 1024;
+  static constexpr int kTmemCols = 256;
+  static_assert(D + 2 * kPage <= kTmemCols, "O and two S");
+};
+
+struct BigMisc {
+  unsigned long long bad[2];  // drafted keys of a tile whose value is not finite
+  uint32_t tmem_base;
+  int abort;
+  int bad_page[8];  // e4m3: the slot's page id was out of range
+};
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(BigCfg<D, E4M3>::kThreads, 2)
+    tree_rows128_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const TreeLaunch a) {
+  using C = BigCfg<D, E4M3>;
+  static_assert(sizeof(BigMisc) <= 64 && C::kRing <= 8, "misc layout");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  BigMisc* misc = reinterpret_cast<BigMisc*>(smem + C::kOffMisc);
+  volatile int* abort_flag = &misc->abort;
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto b_full = [&](int s) { return bar0 + 8u * s; };
+  auto b_empty = [&](int s) { return bar0 + 8u * (C::kRing + s); };
+  const uint32_t bar1 = bar0 + 16u * C::kRing;
+  const uint32_t b_q_full = bar1;
+  auto b_s_full = [&](int i) { return bar1 + 8u * (1 + i); };
+  auto b_p_full = [&](int i) { return bar1 + 8u * (3 + i); };
+  const uint32_t b_pv_done = bar1 + 8u * 5;
+  const uint32_t b_o_final = bar1 + 8u * 6;
+  // V of the CTA's i-th tile with drafted keys is checked; bf16: has landed
+  auto b_checked = [&](int i) { return bar1 + 8u * (7 + i); };
+  auto b_drafted = [&](int i) { return bar1 + 8u * (9 + i); };
+  // e4m3: K (0) or V (1) is converted, its MMAs are done
+  auto b_ready = [&](int v) { return bar1 + 8u * (9 + v); };
+  auto b_free = [&](int v) { return bar1 + 8u * (11 + v); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x;
+  const int kv = blockIdx.y % a.Hkv, rb = blockIdx.y / a.Hkv;
+  const int b = blockIdx.z;
+  const int g = a.Hq / a.Hkv;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  const Seq sq = seq_of(a.cu_q, a.seq_lens, b, a.max_q, a.total_q, a.L, a.max_pages);
+  const int row0 = rb * kMmaRows;
+  const int rows = min(kMmaRows, sq.T * g - row0);
+  if (rows <= 0) return;
+  const int t_begin = split * (a.split_len / kPage);
+  const int t_end = min((sq.len + kPage - 1) / kPage, t_begin + a.split_len / kPage);
+  const int nt = t_end - t_begin;
+  auto out_row = [&](int r) {
+    const int t = (row0 + r) / g;
+    return static_cast<size_t>(sq.tok0 + t) * a.Hq + kv * g + (row0 + r) - t * g;
+  };
+  if (nt <= 0) {
+    if (a.n_splits > 1) {
+      for (int r = threadIdx.x; r < rows; r += C::kThreads)
+        a.lse_part[out_row(r) * a.n_splits + split] = NEG_INF;
+    } else {
+      for (int i = threadIdx.x; i < rows * D; i += C::kThreads)
+        static_cast<__nv_bfloat16*>(a.o)[out_row(i / D) * D + i % D] = __float2bfloat16_rn(0.f);
+    }
+    return;
+  }
+  // tiles from jt0 on hold drafted keys (at most two) or end past the last key
+  const int jt0 = sq.prefix / kPage - t_begin;
+  const int active = (rows + 31) / 32;  // softmax warps with a row
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kRing; ++s) {
+      mbar_init(b_full(s), 1);
+      mbar_init(b_empty(s), E4M3 ? C::kPrep : 1);
+    }
+    mbar_init(b_q_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_s_full(i), 1);
+      mbar_init(b_p_full(i), active);
+      mbar_init(b_checked(i), C::kPrep);
+      if constexpr (E4M3) {
+        mbar_init(b_ready(i), C::kPrep);
+        mbar_init(b_free(i), 1);
+      } else {
+        mbar_init(b_drafted(i), 1);
+      }
+      misc->bad[i] = 0;
+    }
+    mbar_init(b_pv_done, 1);
+    mbar_init(b_o_final, 1);
+    misc->abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&misc->tmem_base), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tO = misc->tmem_base;
+  auto tS = [&](int i) { return tO + D + i * kPage; };
+  auto give_up = [&](int site) {
+    *abort_flag = 1;
+    atomicCAS(a.status, 0, ATTN_DEVICE_TIMEOUT_BASE + site);
+  };
+
+  // The ring's sequence is the order of use: K_0, K_1, V_0, K_2, V_1, ...,
+  // V_last.  Item i: V of tile i/2 - 1 for even i >= 2 (and for the last one),
+  // else K of tile (i + 1) / 2.
+  const int n_items = 2 * nt;
+  auto item_of = [&](int i, int& tile) {  // returns whether it is a V tile
+    if (i == n_items - 1) {
+      tile = nt - 1;
+      return true;
+    }
+    if (i == 0 || (i & 1)) {
+      tile = (i + 1) / 2;
+      return false;
+    }
+    tile = i / 2 - 1;
+    return true;
+  };
+  auto item_k = [&](int tile) { return tile == 0 ? 0 : 2 * tile - 1; };
+  auto item_v = [&](int tile) { return tile == nt - 1 ? n_items - 1 : 2 * tile + 2; };
+
+  if (warp == 0) {
+    // ------------------------------------------------ copies
+    const int* table = a.block_table + static_cast<size_t>(b) * a.max_pages + t_begin;
+    int pages_k = 0, pages_v = 0;  // lane i: the page of tile i + 32 n, for the K and the V stream
+    int issued = 0, drafted = 0;
+    bool ok = true;
+    for (int i = 0; i < n_items && ok; ++i) {
+      int tile;
+      const bool is_v = item_of(i, tile);
+      if ((tile & 31) == 0) {
+        const int p = tile + lane < nt ? table[tile + lane] : -1;
+        if (is_v)
+          pages_v = p;
+        else
+          pages_k = p;
+      }
+      const int page = __shfl_sync(kFull, is_v ? pages_v : pages_k, tile & 31);
+      const int s = i % C::kRing;
+      if (lane == 0) {
+        if (i >= C::kRing)
+          ok = mbar_wait(b_empty(s), ((i / C::kRing) - 1) & 1, abort_flag, a.wait_limit_ns);
+        if (ok) {
+          const bool good = page >= 0 && page < a.num_pages;
+          const long long grp = static_cast<long long>(good ? page : a.num_pages) * a.Hkv + kv;
+          const uint32_t dst = sbase + C::kOffRing + s * C::kSlot;
+          if constexpr (E4M3) {
+            misc->bad_page[s] = good ? 0 : 1;  // reads zeros
+            mbar_arrive_expect_tx(b_full(s), good ? C::kRaw + kPage * 4 : 0);
+            if (good) {
+              bulk_load(dst, static_cast<const uint8_t*>(is_v ? a.V : a.K) + grp * C::kRaw, C::kRaw, b_full(s));
+              bulk_load(sbase + C::kOffScale + s * (kPage * 4), (is_v ? a.v_scales : a.k_scales) + grp * kPage,
+                        kPage * 4, b_full(s));
+            }
+          } else {  // a page id out of range: the box lies past the pool's end and reads zeros
+            uint32_t bar = b_full(s);
+            if (is_v && tile >= jt0) {  // the MMA issuer waits for the check instead
+              bar = b_drafted(tile - max(jt0, 0));
+              mbar_arrive(b_full(s));
+              drafted = tile - max(jt0, 0) + 1;
+            }
+            mbar_arrive_expect_tx(bar, C::kTile);
+#pragma unroll
+            for (int p = 0; p < C::kPanels; ++p)
+              tma_load_3d(dst + p * C::kTilePanel, is_v ? &tmV : &tmK, bar, p * 64, 0, static_cast<int>(grp));
+          }
+          ++issued;
+        }
+      }
+      ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+    }
+    if (lane == 0) {
+      if (!ok) give_up(40);
+      for (int i = max(0, issued - C::kRing); i < issued; ++i)  // no copy in flight at the end
+        mbar_drain(b_full(i % C::kRing), (i / C::kRing) & 1, a.wait_limit_ns);
+      for (int i = 0; i < drafted; ++i) mbar_drain(b_drafted(i), 0, a.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16_f32(kMmaRows, kPage, false, false);
+      constexpr uint32_t idPV = idesc_bf16_f32(kMmaRows, D, false, true);
+      auto wait = [&](uint32_t bar, int parity, int site) {
+        if (mbar_wait(bar, parity, abort_flag, a.wait_limit_ns)) return true;
+        give_up(site);
+        return false;
+      };
+      bool ok = wait(b_q_full, 0, 41);
+      for (int j = 0; ok && j <= nt; ++j) {
+        if (j < nt) {
+          const int i = item_k(j), s = i % C::kRing;
+          const uint32_t sK = sbase + (E4M3 ? C::kOffConv : C::kOffRing + s * C::kSlot);
+          if (!(ok = E4M3 ? wait(b_ready(0), j & 1, 42) : wait(b_full(s), (i / C::kRing) & 1, 42))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk & 3) * 32;  // 16 bf16 = 32 B inside a 128 B row
+            mma_ss(tS(j & 1), sw128_desc(sbase + C::kOffQ + (kk >> 2) * C::kQPanel + off, 16, 1024),
+                   sw128_desc(sK + (kk >> 2) * C::kTilePanel + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(b_s_full(j & 1));
+          mma_commit(E4M3 ? b_free(0) : b_empty(s));
+        }
+        if (j >= 1) {
+          const int t = j - 1, i = item_v(t), s = i % C::kRing;
+          const uint32_t sV = sbase + (E4M3 ? C::kOffConv + C::kTile : C::kOffRing + s * C::kSlot);
+          if (!(ok = E4M3 ? wait(b_ready(1), t & 1, 43) : wait(b_full(s), (i / C::kRing) & 1, 43))) break;
+          if (!E4M3 && t >= jt0 && !(ok = wait(b_checked(t - max(jt0, 0)), 0, 44))) break;
+          if (!(ok = wait(b_p_full(t & 1), (t >> 1) & 1, 45))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kPage / 16; ++kk)
+            mma_ts(tO, tS(t & 1) + kk * 8, sw128_desc(sV + kk * 16 * 128, C::kTilePanel, 1024), idPV,
+                   (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(E4M3 ? b_free(1) : b_empty(s));
+          mma_commit(b_pv_done);
+        }
+      }
+      mma_commit(b_o_final);
+      mbar_drain(b_o_final, 0, a.wait_limit_ns);  // MMAs finish before TMEM is released
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------ softmax
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const bool valid = r < rows;
+    const int tok = valid ? (row0 + r) / g : 0;
+    {  // this row of Q into the swizzled operand
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                        (valid ? out_row(r) : 0) * D);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 u = valid ? src[c] : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(smem + C::kOffQ + (c >> 3) * C::kQPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_q_full);
+    }
+    uint64_t bits = 0;
+    if (valid) bits = a.mask ? a.mask[sq.tok0 + tok] : (tok >= 63 ? ~0ull : (2ull << tok) - 1);
+    float m_ref = NEG_INF, l_sum = 0.f;
+    bool ok = true;
+    if ((warp & 3) < active) {
+      for (int j = 0; j < nt; ++j) {
+        const int sb = j & 1;
+        if (!__all_sync(kFull, mbar_wait(b_s_full(sb), (j >> 1) & 1, abort_flag, a.wait_limit_ns))) {
+          if (lane == 0) give_up(46);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t x[kPage];
+        tmem_ld_row<kPage>(tS(sb) + lane_off, x);
+        tmem_wait_ld();
+        const bool tail = j >= jt0;
+        uint64_t bad = 0;
+        if (tail) {
+          // which of the 64 keys this row sees
+          const int key0 = (t_begin + j) * kPage;
+          const int n_prefix = min(max(sq.prefix - key0, 0), kPage), n_len = min(sq.len - key0, kPage);
+          uint64_t sees = n_prefix >= 64 ? ~0ull : (1ull << n_prefix) - 1;
+          const int first = key0 - sq.prefix;  // drafted index of the tile's first key
+          const uint64_t drafted = first >= 64 ? 0 : first >= 0 ? bits >> first : first > -64 ? bits << -first : 0;
+          sees |= drafted;
+          if (n_len < 64) sees &= (1ull << n_len) - 1;
+#pragma unroll
+          for (int c = 0; c < kPage; ++c)
+            if (!((sees >> c) & 1)) x[c] = 0xff800000u;
+          const int jt = j - max(jt0, 0);
+          if (!__all_sync(kFull, mbar_wait(b_checked(jt), 0, abort_flag, a.wait_limit_ns))) {
+            if (lane == 0) give_up(47);
+            ok = false;
+            break;
+          }
+          bad = *reinterpret_cast<volatile unsigned long long*>(&misc->bad[jt]) & sees;
+        }
+        float mt = NEG_INF;
+#pragma unroll
+        for (int c = 0; c < kPage; c += 2) mt = fmax3(mt, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        mt *= a.scale_log2;
+        const bool moved = mt > m_ref + kRefSlack;
+        float alpha = 1.f;
+        if (moved) {
+          alpha = ex2(m_ref - mt);  // m_ref = -inf gives 0
+          m_ref = mt;
+        }
+        const float base = m_ref == NEG_INF ? 0.f : m_ref;
+        if (__any_sync(kFull, moved && j > 0)) {
+          // O is read and written back: the last P V must have finished
+          if (!__all_sync(kFull, mbar_wait(b_pv_done, (j - 1) & 1, abort_flag, a.wait_limit_ns))) {
+            if (lane == 0) give_up(48);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(tO + lane_off + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tmem_st16(tO + lane_off + c0, o);
+          }
+        }
+        // P = 2^(x - ref) as bf16 over the scores; the sum adds the rounded values
+        float rs = 0.f;
+#pragma unroll
+        for (int c0 = 0; c0 < kPage; c0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float p0 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c]), a.scale_log2, -base));
+            float p1 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c + 1]), a.scale_log2, -base));
+            const uint32_t w = pack_bf16x2(p0, p1);
+            rs += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
+            pk[c] = w;
+          }
+          if (bad) {  // a value that is not finite was taken out of V: NaN for whoever sees it
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              if ((bad >> (c0 + 2 * c)) & 1) pk[c] = (pk[c] & 0xffff0000u) | 0x7fc0u;
+              if ((bad >> (c0 + 2 * c + 1)) & 1) pk[c] = (pk[c] & 0xffffu) | 0x7fc00000u;
+            }
+          }
+          tmem_st16(tS(sb) + lane_off + c0 / 2, pk);
+        }
+        l_sum = l_sum * alpha + rs;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p_full(sb));
+      }
+      // ---- O / l
+      if (__all_sync(kFull, ok && mbar_wait(b_o_final, 0, abort_flag, a.wait_limit_ns) && !*abort_flag)) {
+        tc_fence_after();
+        const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;  // a row that sees nothing here
+        const size_t at = valid ? out_row(r) : 0;
+        float* part = a.o_part + (at * a.n_splits + split) * D;
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + at * D;
+        if (valid && a.n_splits > 1)
+          a.lse_part[at * a.n_splits + split] = l_sum == 0.f ? NEG_INF : m_ref + __log2f(l_sum);
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t o[16];
+          tmem_ld16(tO + lane_off + c0, o);
+          tmem_wait_ld();
+          if (!valid) continue;
+          float f[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) f[c] = l_sum == 0.f ? 0.f : __uint_as_float(o[c]) * inv;
+          if (a.n_splits > 1) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 4)
+              *reinterpret_cast<float4*>(part + c0 + c) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; c += 8)
+              *reinterpret_cast<uint4*>(orow + c0 + c) =
+                  make_uint4(pack_bf16x2(f[c], f[c + 1]), pack_bf16x2(f[c + 2], f[c + 3]),
+                             pack_bf16x2(f[c + 4], f[c + 5]), pack_bf16x2(f[c + 6], f[c + 7]));
+          }
+        }
+      } else if (valid) {  // a wait gave up: no weight in the merge
+        const size_t at = out_row(r);
+        if (a.n_splits > 1)
+          a.lse_part[at * a.n_splits + split] = NEG_INF;
+        else
+          for (int c = 0; c < D; ++c) static_cast<__nv_bfloat16*>(a.o)[at * D + c] = __float2bfloat16_rn(0.f);
+      }
+    }
+  } else {
+    // ------------------------------------------------ tiles
+    const int t = threadIdx.x - 6 * 32;
+    constexpr int kN = C::kPrep * 32;
+    bool ok = true;
+    if constexpr (E4M3) {
+      for (int i = 0; i < n_items; ++i) {
+        int j;
+        const int is_v = item_of(i, j) ? 1 : 0;
+        const int s = i % C::kRing;
+        bool got = mbar_wait(b_full(s), (i / C::kRing) & 1, abort_flag, a.wait_limit_ns);
+        if (got && j > 0) got = mbar_wait(b_free(is_v), (j - 1) & 1, abort_flag, a.wait_limit_ns);
+        if (!__all_sync(kFull, got)) {
+          ok = false;
+          break;
+        }
+        const uint32_t src = sbase + C::kOffRing + s * C::kSlot;
+        const uint32_t scales = sbase + C::kOffScale + s * (kPage * 4);
+        const uint32_t dst = sbase + C::kOffConv + is_v * C::kTile;
+        const bool zero = misc->bad_page[s] != 0;
+        const int key0 = (t_begin + j) * kPage;
+        constexpr int kChunks = D / 16;  // 16-code chunks of a key
+#pragma unroll
+        for (int n = 0; n < kPage * kChunks / kN; ++n) {
+          const int chunk = n * kN + t, key = chunk / kChunks, c = chunk % kChunks;
+          const uint4 u = lds128(src + chunk * 16);
+          const float sc = lds_f32(scales + key * 4);
+          const uint32_t f = pack_bf16x2(sc, sc);  // a power of two: exact
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[2 * e] = mul_bf16x2(e4m3_hi_to_bf16x2(__byte_perm(w[e], 0, 0x1000)), f);
+            o[2 * e + 1] = mul_bf16x2(e4m3_hi_to_bf16x2(__byte_perm(w[e], 0, 0x3020)), f);
+          }
+          bool clear = zero;
+          if (is_v && j >= jt0) {
+            clear |= key0 + key >= sq.len;
+            bool nf = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) nf |= has_nonfinite(o[e]);
+            if (nf && !clear && key0 + key >= sq.prefix) {
+              clear = true;
+              atomicOr(&misc->bad[j - max(jt0, 0)], 1ull << key);
+            }
+          }
+          if (clear) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 0;
+          }
+          // two 16-byte chunks of the bf16 row; the upper half of the row's
+          // threads store theirs in the other order, so that eight
+          // neighbours meet eight different banks
+          const uint32_t row = dst + (c >> 2) * C::kTilePanel + key * 128;
+          const int flip = (c >> 2) & 1, c2 = 2 * (c & 3);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int hh = h ^ flip;
+            sts128(row + (((c2 + hh) ^ (key & 7)) << 4), hh ? o[4] : o[0], hh ? o[5] : o[1], hh ? o[6] : o[2],
+                   hh ? o[7] : o[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(b_empty(s));
+          mbar_arrive(b_ready(is_v));
+          if (is_v && j >= jt0) mbar_arrive(b_checked(j - max(jt0, 0)));
+        }
+      }
+    } else {
+      // V tiles that hold drafted keys: slots past the end are cleared, and
+      // values that are not finite taken out (softmax makes up for them)
+      for (int j = max(jt0, 0); j < nt; ++j) {
+        const int n = j - max(jt0, 0);
+        if (!__all_sync(kFull, mbar_wait(b_drafted(n), 0, abort_flag, a.wait_limit_ns))) {
+          ok = false;
+          break;
+        }
+        const uint32_t tile = sbase + C::kOffRing + (item_v(j) % C::kRing) * C::kSlot;
+        const int key0 = (t_begin + j) * kPage;
+        for (int chunk = t; chunk < kPage * (D / 8); chunk += kN) {
+          const int key = (chunk / 8) % kPage;
+          const uint32_t at = tile + chunk * 16;  // panels of [64][128 B]: the swizzle stays inside a row
+          const uint4 u = lds128(at);
+          const bool nf = has_nonfinite(u.x) || has_nonfinite(u.y) || has_nonfinite(u.z) || has_nonfinite(u.w);
+          const bool past = key0 + key >= sq.len;
+          if (past || (nf && key0 + key >= sq.prefix)) {
+            sts128(at, 0, 0, 0, 0);
+            if (!past) atomicOr(&misc->bad[n], 1ull << key);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_checked(n));
+      }
+    }
+    if (!ok && lane == 0) give_up(49);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tO, C::kTmemCols);
+  }
+}
+
 // Exact merge of the splits: one warp a row, D/32 columns a lane.
 template <int D>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeLaunch a) {
@@ -620,9 +1149,36 @@ int launch_rows16(const TreeLaunch& a) {
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+template <int D, bool E4M3>
+int launch_rows128(const TreeLaunch& a) {
+  using C = BigCfg<D, E4M3>;
+  auto kern = tree_rows128_kernel<D, E4M3>;
+  static uint64_t attr_done = 0;  // one bit per device ordinal
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return ATTN_ERR_CUDA;
+  if (!(attr_done >> dev & 1)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    attr_done |= uint64_t(1) << dev;
+  }
+  CUtensorMap mk{}, mv{};  // the e4m3 pages are copied without one
+  const int groups = a.num_pages * a.Hkv;
+  if (!E4M3 && (!tma_map_bhnd(&mk, a.K, groups, kPage, D, kPage) || !tma_map_bhnd(&mv, a.V, groups, kPage, D, kPage)))
+    return ATTN_ERR_CUDA;
+  const int rbs = (a.max_q * (a.Hq / a.Hkv) + kMmaRows - 1) / kMmaRows;
+  kern<<<dim3(a.n_splits, a.Hkv * rbs, a.B), C::kThreads, C::kSmem, a.stream>>>(mk, mv, a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Rows of a CTA: 16 where all rows of a KV head fit (a decode of single tokens
+// with up to 16 query heads a group), else 128.
+int rows_of(int max_q, int g) { return max_q * static_cast<long long>(g) <= kRows ? kRows : kMmaRows; }
+
 template <int D>
 int launch_d(const TreeLaunch& a) {
-  const int st = a.k_scales ? launch_rows16<D, true>(a) : launch_rows16<D, false>(a);
+  const bool few = rows_of(a.max_q, a.Hq / a.Hkv) == kRows;
+  const int st = a.k_scales ? (few ? launch_rows16<D, true>(a) : launch_rows128<D, true>(a))
+                            : (few ? launch_rows16<D, false>(a) : launch_rows128<D, false>(a));
   if (st != ATTN_OK || a.n_splits == 1) return st;
   tree_merge_kernel<D><<<dim3((a.max_q * a.Hq + 3) / 4, a.B), 128, 0, a.stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
@@ -631,7 +1187,8 @@ int launch_d(const TreeLaunch& a) {
 // Keys of a split: waves of the 296 resident CTAs (148 SMs x 2) times (tiles of
 // a CTA + about 4 tiles' worth of start, merge and partial results).
 int split_len_of(int B, int max_q, int Hq, int Hkv, int L) {
-  const long long groups = static_cast<long long>(B) * Hkv * ((static_cast<long long>(max_q) * (Hq / Hkv) + kRows - 1) / kRows);
+  const int per = rows_of(max_q, Hq / Hkv);
+  const long long groups = static_cast<long long>(B) * Hkv * ((static_cast<long long>(max_q) * (Hq / Hkv) + per - 1) / per);
   const int n_tiles = (L + kPage - 1) / kPage;
   int best = n_tiles;
   long long best_cost = -1;
