@@ -96,21 +96,18 @@ struct TreeLaunch {
   void* o;
   int B, max_q, total_q, Hq, Hkv, num_pages, max_pages, L, d;
   float scale_log2;
-  int split_len;  // keys per split, a multiple of kDecodeTile
-  int n_splits;
-  float* o_part;    // [total_q * Hq, n_splits, d] fp32, with n_splits > 1
-  float* lse_part;  // [total_q * Hq, n_splits]
+  int planes;     // row blocks of the longest draft: grid.y
+  int ctas;       // CTAs of a plane: grid.x
+  int min_tiles;  // least work of a CTA
+  float* part;    // [planes, ctas, 2, rows of a CTA, d] fp32: shares of a KV head's keys
+  float* lse;     // [planes, ctas, 2, rows of a CTA]
   int* status;
   unsigned long long wait_limit_ns;
   cudaStream_t stream;
 };
 
-int launch_tree(const TreeLaunch& a);
-
-// Tensor map over a pool of e4m3 codes [groups, 64, D], d fastest: boxes of a
-// whole group (64 keys), rows swizzled as 128 bytes (D = 128) or 64 (D = 64);
-// groups past the end read as zeros.
-bool tma_map_codes(CUtensorMap* m, const void* base, long long groups, int D);
+int launch_tree_rows16(const TreeLaunch& a);   // tree_rows16_sm100.cu
+int launch_tree_rows128(const TreeLaunch& a);  // tree_rows128_sm100.cu
 
 // Current device (sm_100 checked) and its device status word (api.cu).
 int device_context(int* dev, int** status);

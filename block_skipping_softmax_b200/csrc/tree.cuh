@@ -1,0 +1,248 @@
+// What the tree-attention kernels share: the sequences, the distribution of
+// their work, and small helpers.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace bss {
+
+constexpr int kPage = kDecodeTile;  // 64 keys: one page, one tile
+constexpr int kFewRows = 16;        // rows of a CTA of the two kernels
+constexpr int kManyRows = 128;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kRefSlack = 8.f;  // log2 units: the reference maximum lags by less, so p < 2^8
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ bool has_nonfinite(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u) || ((w & 0x7f800000u) == 0x7f800000u);
+}
+
+// ---- e4m3 codes in registers ------------------------------------------------
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// Two codes in the upper bytes of the halfwords of w (the lower bytes may hold
+// anything) to two bf16: sign, exponent and mantissa move to their bf16
+// places, and 2^120 moves the exponent's bias from 7 to 127, subnormal codes
+// included.  Exact.  The NaN code (0x7f) comes out as 480: the writer never
+// stores it under a finite scale, and a NaN scale makes the value NaN.
+__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t w) {
+  return mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07f007f0u), 0x7b807b80u);
+}
+
+// Four codes (bytes of w) to two pairs of fp16, in order.  Exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Queries meet e4m3 keys as fp16, since the codes become fp16 in one
+// instruction a pair.  A row is scaled by the power of two that brings its
+// largest element to [2^14, 2^15): bf16's 8 bits fit in fp16's 11, so every
+// element within 2^-28 of the largest is exact, and a smaller one is off by at
+// most 2^-40 of the largest.  Returns the factor's exponent; 0 for a row of
+// zeros or with inf or NaN.
+__device__ __forceinline__ int f16_shift(uint32_t amax_bits) {
+  if (amax_bits == 0 || amax_bits >= 0x7f800000u) return 0;
+  return min(14 + 127 - static_cast<int>(amax_bits >> 23), 126);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Values of an e4m3 cache are fp16 operands too where that is exact: a code
+// (a multiple of 2^-9 up to 448) times a scale from 2^-15 to 2^7 has a place in
+// fp16.  A tile with a scale outside of that takes bf16 operands, at more
+// instructions a code.  Probabilities carry 2^7, so that fp16 (up to 65504)
+// holds them from p = 2^8 down to 2^-31 of the reference maximum.
+constexpr int kPShift = 7;
+__device__ __forceinline__ bool fits_f16(float scale) { return scale >= pow2(-15) && scale <= pow2(7); }
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// ---- sequences and work -----------------------------------------------------
+
+struct Seq {
+  int tok0, T;      // first row of the packed batch, tokens
+  int len, prefix;  // keys; keys that every token sees
+};
+
+__device__ __forceinline__ Seq seq_of(const TreeLaunch& a, int b) {
+  Seq s;
+  const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), n = __ldg(a.seq_lens + b);
+  s.tok0 = min(max(c0, 0), a.total_q);
+  s.T = min(min(max(c1, s.tok0), a.total_q) - s.tok0, a.max_q);
+  s.len = max(0, min(min(n, a.L), a.max_pages * kPage));
+  s.prefix = max(0, s.len - s.T);
+  return s;
+}
+
+// The work of one plane (row block `plane` of every sequence that has one) is
+// the line of all its tiles: sequences, KV heads and tiles, in this order.  Its
+// CTAs take equal pieces of that line, whatever the sequences' lengths, so a
+// ragged batch keeps every SM busy to the end.  A piece consists of segments,
+// runs of tiles of one KV head; a segment that is not all of its KV head's
+// tiles leaves a share of the result in one of the CTA's two places (only its
+// first and its last segment can be one), which tree_merge_kernel adds up.  A
+// sequence without keys counts as one tile, so that its zeros get written.
+//
+// Planes run side by side over the same line, so that row blocks that read the
+// same pages do so at about the same time, from L2.
+// A plane has fewer than 2^31 tiles (the host checks B * max_seq_len * Hkv).
+struct Line {
+  int w, incl, before;  // this lane's sequence of the chunk, sum up to it, sum before the chunk
+  int chunk;
+
+  __device__ __forceinline__ static int work_of(const TreeLaunch& a, const Seq& s, int first_row) {
+    if (s.T * (a.Hq / a.Hkv) <= first_row) return 0;
+    return max(1, (s.len + kPage - 1) / kPage) * a.Hkv;
+  }
+  // Warp-collective: 32 sequences from `at` on.
+  __device__ __forceinline__ void load(const TreeLaunch& a, int first_row, int at, int sum) {
+    const int lane = threadIdx.x & 31;
+    chunk = at;
+    before = sum;
+    w = 0;
+    if (at + lane < a.B) w = work_of(a, seq_of(a, at + lane), first_row);
+    incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += x;
+    }
+  }
+  __device__ __forceinline__ int total() const { return __shfl_sync(kFull, incl, 31); }
+};
+
+// How W tiles are divided among CTAs: `used` of them, the first `more` with one
+// tile more than the others' `each`.
+struct Pieces {
+  int used, each, more;
+  __device__ __forceinline__ Pieces(const TreeLaunch& a, int W) {
+    used = max(1, min(a.ctas, (W - 1) / a.min_tiles + 1));
+    each = W / used;
+    more = W - each * used;
+  }
+  __device__ __forceinline__ int first(int cta) const { return each * cta + min(cta, more); }
+  __device__ __forceinline__ int cta_of(int tile) const {
+    const int split = (each + 1) * more;
+    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
+  }
+};
+
+struct Segment {
+  int b, kv;
+  int t0, nt;      // tiles [t0, t0 + nt) of the sequence
+  int row0, rows;  // rows of this plane: row r is token (row0 + r) / g, head (row0 + r) % g of the group
+  bool whole;      // all tiles: the result is final
+  int place;       // else where the share goes: 0 (the CTA's first segment) or 1
+  Seq s;
+};
+
+// The segments of this CTA, for every warp by itself (all calls warp-collective).
+struct Segments {
+  Line line;
+  int begin, pos, end;
+
+  __device__ __forceinline__ void start(const TreeLaunch& a, int per) {
+    const int row0 = blockIdx.y * per;
+    line.load(a, row0, 0, 0);
+    int W = line.total();
+    if (a.B > 32) {
+      for (int at = 32; at < a.B; at += 32) {
+        line.load(a, row0, at, W);
+        W += line.total();
+      }
+      line.load(a, row0, 0, 0);
+    }
+    begin = pos = end = 0;
+    if (W == 0) return;
+    const Pieces p(a, W);
+    if (static_cast<int>(blockIdx.x) < p.used) {
+      begin = pos = p.first(blockIdx.x);
+      end = p.first(blockIdx.x + 1);
+    }
+  }
+  __device__ __forceinline__ bool next(const TreeLaunch& a, int per, Segment& g) {
+    if (pos >= end) return false;
+    const int row0 = blockIdx.y * per;
+    while (pos >= line.before + line.total()) line.load(a, row0, line.chunk + 32, line.before + line.total());
+    const int l = __ffs(__ballot_sync(kFull, pos < line.before + line.incl)) - 1;
+    const int first = line.before + __shfl_sync(kFull, line.incl - line.w, l);
+    g.b = line.chunk + l;
+    g.s = seq_of(a, g.b);
+    const int tiles = (g.s.len + kPage - 1) / kPage, span = max(1, tiles);
+    g.kv = (pos - first) / span;
+    g.t0 = pos - first - g.kv * span;
+    const int n = min(span - g.t0, end - pos);
+    g.nt = min(n, tiles - g.t0);
+    g.whole = n == span;
+    g.place = pos == begin ? 0 : 1;
+    g.row0 = row0;
+    g.rows = min(per, g.s.T * (a.Hq / a.Hkv) - row0);
+    pos += n;
+    return true;
+  }
+};
+
+// Row r of a segment: its row of q and o, [total_q * Hq].
+__device__ __forceinline__ size_t row_at(const TreeLaunch& a, const Segment& g, int r, int* token = nullptr) {
+  const int group = a.Hq / a.Hkv;
+  const int t = (g.row0 + r) / group;
+  if (token) *token = t;
+  return static_cast<size_t>(g.s.tok0 + t) * a.Hq + g.kv * group + (g.row0 + r) - t * group;
+}
+// its row of part and lse
+__device__ __forceinline__ size_t share_at(const TreeLaunch& a, int per, int plane, int cta, int place, int r) {
+  return ((static_cast<size_t>(plane) * a.ctas + cta) * 2 + place) * per + r;
+}
+// drafted keys that token t sees
+__device__ __forceinline__ uint64_t bits_of(const TreeLaunch& a, const Seq& s, int t) {
+  return a.mask ? a.mask[s.tok0 + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
+}
+
+// Tensor map over a pool of e4m3 codes [groups, 64, D], d fastest: boxes of a
+// whole group (64 keys), rows swizzled as 128 bytes (D = 128) or 64 (D = 64);
+// groups past the end read as zeros.
+bool tma_map_codes(CUtensorMap* m, const void* base, long long groups, int D);
+
+}  // namespace bss

@@ -1,0 +1,727 @@
+// Tree attention for many rows a KV head: 128 rows a CTA on tcgen05.
+//
+//   warp 0       copies: K and V pages, a ring in shared memory
+//   warp 1       TMEM, and the one thread that issues the MMAs:
+//                  S_j = Q K_j^T (two buffers), O += P_j V_j (P read from TMEM)
+//   warps 4-7    softmax: a thread owns the row of TMEM lane 32 (warp % 4) + lane
+//   tile warps   bf16 pool: warps 2 and 3 check the V tiles that hold drafted
+//                keys.  e4m3: warps 8-11 turn codes of K into an fp16 operand and
+//                warps 12-15 codes of V into an fp16 (rarely bf16) one; the
+//                registers are divided anew between the roles
+//
+// A tile is one page of 64 keys, so that TMEM holds O and two S in 256 columns
+// and two CTAs share an SM: one's softmax runs beside the other's MMAs.  Every
+// role runs through the CTA's segments by itself; the ring, the MMAs and the
+// conversion go on across their borders.  Rows past the last one are zero
+// queries, and softmax warps without a row only keep step.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "tree.cuh"
+
+namespace bss {
+
+namespace {
+
+constexpr int kRows = kManyRows;
+constexpr int kChecks = 4;  // tiles with drafted keys on their way: see Tails
+
+template <int D, bool E4M3>
+struct Cfg {
+  static constexpr int kPrep = E4M3 ? 4 : 2;  // warps that convert K, convert V or check V tiles
+  static constexpr int kPrepWarp = E4M3 ? 8 : 2;
+  static constexpr int kThreads = E4M3 ? 512 : 256;
+  // Registers a thread, e4m3: 64 at launch, then by warpgroup (copies and MMAs,
+  // softmax, tiles, tiles), 256 in all.
+  static constexpr int kRegs = 64, kRegsIssue = 40, kRegsSoftmax = 104, kRegsPrep = 56;
+  static constexpr int kQPanel = kRows * 128;
+  static constexpr int kTile = kPage * D * 2;  // K or V of a page as 16-bit values
+  static constexpr int kTilePanel = kPage * 128;
+  static constexpr int kRaw = kPage * D;       // as codes
+  static constexpr int kRing = E4M3 ? (D == 128 ? 5 : 8) : (D == 128 ? 4 : 6);  // tiles in flight
+  static constexpr int kSlot = E4M3 ? kRaw : kTile;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffConv = kOffQ + kRows * D * 2;           // e4m3: K and V operands
+  static constexpr int kOffRing = kOffConv + (E4M3 ? 2 * kTile : 0);
+  static constexpr int kScaleBytes = E4M3 ? 2 * kPage * 4 : 0;    // K (a K tile's slot only), V
+  static constexpr int kOffScale = kOffRing + kRing * kSlot;       // e4m3: [slot][K, V][64] floats
+  static constexpr int kOffKScale = kOffScale + kRing * kScaleBytes;  // e4m3: [4][64], for softmax
+  static constexpr int kOffBar = kOffKScale + (E4M3 ? 4 * kPage * 4 : 0);
+  // full[ring], empty[ring], q_full, s_full[2], p_full[2], pv_done, o_final,
+  // checked[4]; bf16: drafted[4]; e4m3: ready[K, V], free[K, V]
+  static constexpr int kBars = 2 * kRing + 7 + 2 * kChecks;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;
+  static constexpr int kMiscBytes = 224;
+  static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;
+  static constexpr int kTmemCols = 256;
+  static_assert(D + 2 * kPage <= kTmemCols, "O and two S");
+};
+
+struct Misc {
+  unsigned long long bad[kChecks][4];  // by tile warp: drafted keys of a tile whose value is not finite
+  uint32_t tmem_base;
+  int abort;
+  int bad_page[8];  // e4m3: the slot's page id was out of range
+  int f16[4][2];    // e4m3, by tile: whether V (keys 0-31, 32-63) is an fp16 operand
+};
+
+// kind::f16 with fp16 A and B (format 0), fp32 accumulation, A K-major
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The ring's sequence within a segment of nt tiles is the order of use:
+// K_0, K_1, V_0, K_2, V_1, ..., V_last.
+__device__ __forceinline__ int item_k(int tile) { return tile == 0 ? 0 : 2 * tile - 1; }
+__device__ __forceinline__ int item_v(int tile, int nt) { return tile == nt - 1 ? 2 * nt - 1 : 2 * tile + 2; }
+__device__ __forceinline__ bool item_is_v(int i, int nt, int& tile) {
+  if (i == 2 * nt - 1) {
+    tile = nt - 1;
+    return true;
+  }
+  const bool v = i >= 2 && (i & 1) == 0;
+  tile = v ? i / 2 - 1 : (i + 1) / 2;
+  return v;
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
+    tree_rows128_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeLaunch a) {
+  using C = Cfg<D, E4M3>;
+  static_assert(sizeof(Misc) <= C::kMiscBytes && C::kRing <= 8 && C::kPrep <= 4, "misc layout");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  Misc* misc = reinterpret_cast<Misc*>(smem + C::kOffMisc);
+  volatile int* abort_flag = &misc->abort;
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto b_full = [&](int s) { return bar0 + 8u * s; };
+  auto b_empty = [&](int s) { return bar0 + 8u * (C::kRing + s); };
+  const uint32_t bar1 = bar0 + 16u * C::kRing;
+  const uint32_t b_q_full = bar1;
+  auto b_s_full = [&](int i) { return bar1 + 8u * (1 + i); };
+  auto b_p_full = [&](int i) { return bar1 + 8u * (3 + i); };
+  const uint32_t b_pv_done = bar1 + 8u * 5;
+  const uint32_t b_o_final = bar1 + 8u * 6;
+  // V tile number c with drafted keys (over the CTA's segments) is checked; bf16: has landed
+  auto b_checked = [&](int c) { return bar1 + 8u * (7 + c % kChecks); };
+  auto b_drafted = [&](int c) { return bar1 + 8u * (7 + kChecks + c % kChecks); };
+  // e4m3: K (0) or V (1) is converted, its MMAs are done
+  auto b_ready = [&](int v) { return bar1 + 8u * (7 + kChecks + v); };
+  auto b_free = [&](int v) { return bar1 + 8u * (9 + kChecks + v); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kRing; ++s) {
+      mbar_init(b_full(s), 1);
+      mbar_init(b_empty(s), E4M3 ? C::kPrep : 1);
+    }
+    mbar_init(b_q_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_s_full(i), 1);
+      mbar_init(b_p_full(i), 4);
+      if constexpr (E4M3) {
+        mbar_init(b_ready(i), C::kPrep);
+        mbar_init(b_free(i), 1);
+      }
+    }
+    for (int i = 0; i < kChecks; ++i) {
+      mbar_init(b_checked(i), C::kPrep);
+      if constexpr (!E4M3) mbar_init(b_drafted(i), 1);
+    }
+    mbar_init(b_pv_done, 1);
+    mbar_init(b_o_final, 1);
+    misc->abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&misc->tmem_base), C::kTmemCols);
+    tmem_relinquish();
+  }
+  Segments list;
+  list.start(a, kRows);
+  Segment sg{};
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tO = misc->tmem_base;
+  auto tS = [&](int i) { return tO + D + i * kPage; };
+  auto give_up = [&](int site) {
+    *abort_flag = 1;
+    atomicCAS(a.status, 0, ATTN_DEVICE_TIMEOUT_BASE + site);
+  };
+  // e4m3: V of tile n is an fp16 operand (known once K of tile n is ready)
+  auto f16_tile = [&](int n) {
+    const volatile int* f = misc->f16[n & 3];
+    return (f[0] & f[1]) != 0;
+  };
+  // Tiles from tail0 on hold drafted keys or end past the last key; there are at
+  // most two in a segment.  They are numbered over the CTA's segments.
+  auto tail0 = [&] { return max(sg.s.prefix / kPage - sg.t0, 0); };
+  auto tails = [&] { return max(sg.nt - tail0(), 0); };
+
+  // ------------------------------------------------ copies
+  auto copies = [&] {
+    int issued = 0, checks = 0, landed = 0;  // items, drafted tiles, drafted tiles issued
+    bool ok = true;
+    while (ok && list.next(a, kRows, sg)) {
+      const int* table = a.block_table + static_cast<size_t>(sg.b) * a.max_pages + sg.t0;
+      int pages_k = 0, pages_v = 0;  // lane i: the page of tile i + 32 n, for the K and the V stream
+      const int first_tail = tail0();
+      for (int i = 0; i < 2 * sg.nt && ok; ++i) {
+        int tile;
+        const bool is_v = item_is_v(i, sg.nt, tile);
+        if ((tile & 31) == 0) {
+          const int p = tile + lane < sg.nt ? table[tile + lane] : -1;
+          if (is_v)
+            pages_v = p;
+          else
+            pages_k = p;
+        }
+        const int page = __shfl_sync(kFull, is_v ? pages_v : pages_k, tile & 31);
+        const int s = issued % C::kRing;
+        if (lane == 0) {
+          if (issued >= C::kRing)
+            ok = mbar_wait(b_empty(s), ((issued / C::kRing) - 1) & 1, abort_flag, a.wait_limit_ns);
+          if (ok) {
+            const bool good = page >= 0 && page < a.num_pages;
+            const long long grp = static_cast<long long>(good ? page : a.num_pages) * a.Hkv + sg.kv;
+            const uint32_t dst = sbase + C::kOffRing + s * C::kSlot;
+            // a page id out of range reads zeros: the box lies past the pool's end
+            if constexpr (E4M3) {
+              misc->bad_page[s] = good ? 0 : 1;
+              mbar_arrive_expect_tx(b_full(s), C::kRaw + (good ? (is_v ? 1 : 2) * kPage * 4 : 0));
+              tma_load_3d(dst, is_v ? &tmV : &tmK, b_full(s), 0, 0, static_cast<int>(grp));
+              if (good) {
+                // the value scales come with K too, for the choice of P's type
+                const uint32_t to = sbase + C::kOffScale + s * C::kScaleBytes;
+                if (!is_v) bulk_load(to, a.k_scales + grp * kPage, kPage * 4, b_full(s));
+                bulk_load(to + kPage * 4, a.v_scales + grp * kPage, kPage * 4, b_full(s));
+              }
+            } else {
+              uint32_t bar = b_full(s);
+              if (is_v && tile >= first_tail) {  // the MMA issuer waits for the check instead
+                landed = checks + tile - first_tail + 1;
+                bar = b_drafted(landed - 1);
+                mbar_arrive(b_full(s));
+              }
+              mbar_arrive_expect_tx(bar, C::kTile);
+#pragma unroll
+              for (int p = 0; p < D / 64; ++p)
+                tma_load_3d(dst + p * C::kTilePanel, is_v ? &tmV : &tmK, bar, p * 64, 0, static_cast<int>(grp));
+            }
+          }
+        }
+        ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+        if (ok) ++issued;
+      }
+      checks += tails();
+    }
+    if (lane == 0) {
+      if (!ok) give_up(40);
+      // no copy in flight at the end
+      for (int i = max(0, issued - C::kRing); i < issued; ++i)
+        mbar_drain(b_full(i % C::kRing), (i / C::kRing) & 1, a.wait_limit_ns);
+      for (int c = max(0, landed - kChecks); !E4M3 && c < landed; ++c)
+        mbar_drain(b_drafted(c), (c / kChecks) & 1, a.wait_limit_ns);
+    }
+  };
+  // ------------------------------------------------ MMA issuer
+  auto issue = [&] {
+    constexpr uint32_t idS = E4M3 ? idesc_f16_f32(kRows, kPage, false) : idesc_bf16_f32(kRows, kPage, false, false);
+    constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true), idPV16 = idesc_f16_f32(kRows, D, true);
+    auto wait = [&](uint32_t bar, int parity, int site) {
+      if (mbar_wait(bar, parity, abort_flag, a.wait_limit_ns)) return true;
+      give_up(site);
+      return false;
+    };
+    bool ok = true;
+    int seg = 0, n0 = 0, item0 = 0, checks = 0;  // segments, tiles, ring items and drafted tiles before this one
+    while (ok && list.next(a, kRows, sg)) {
+      if (lane == 0) {
+        const int nt = sg.nt, first_tail = tail0();
+        ok = wait(b_q_full, seg & 1, 41);
+        for (int j = 0; ok && nt > 0 && j <= nt; ++j) {
+          if (j < nt) {
+            const int n = n0 + j, i = item0 + item_k(j), s = i % C::kRing;
+            const uint32_t sK = sbase + (E4M3 ? C::kOffConv : C::kOffRing + s * C::kSlot);
+            if (!(ok = E4M3 ? wait(b_ready(0), n & 1, 42) : wait(b_full(s), (i / C::kRing) & 1, 42))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk & 3) * 32;  // 16 values = 32 B inside a 128 B row
+              mma_ss(tS(n & 1), sw128_desc(sbase + C::kOffQ + (kk >> 2) * C::kQPanel + off, 16, 1024),
+                     sw128_desc(sK + (kk >> 2) * C::kTilePanel + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(b_s_full(n & 1));
+            mma_commit(E4M3 ? b_free(0) : b_empty(s));
+          }
+          if (j >= 1) {
+            const int t = j - 1, n = n0 + t, i = item0 + item_v(t, nt), s = i % C::kRing;
+            const uint32_t sV = sbase + (E4M3 ? C::kOffConv + C::kTile : C::kOffRing + s * C::kSlot);
+            if (!(ok = E4M3 ? wait(b_ready(1), n & 1, 43) : wait(b_full(s), (i / C::kRing) & 1, 43))) break;
+            if (!E4M3 && t >= first_tail) {
+              const int c = checks + t - first_tail;
+              if (!(ok = wait(b_checked(c), (c / kChecks) & 1, 44))) break;
+            }
+            if (!(ok = wait(b_p_full(n & 1), (n >> 1) & 1, 45))) break;
+            tc_fence_after();
+            const uint32_t id = E4M3 && f16_tile(n) ? idPV16 : idPV;
+#pragma unroll
+            for (int kk = 0; kk < kPage / 16; ++kk)
+              mma_ts(tO, tS(n & 1) + kk * 8, sw128_desc(sV + kk * 16 * 128, C::kTilePanel, 1024), id,
+                     (t > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(E4M3 ? b_free(1) : b_empty(s));
+            mma_commit(b_pv_done);
+          }
+        }
+        mma_commit(b_o_final);
+      }
+      ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+      n0 += sg.nt;
+      item0 += 2 * sg.nt;
+      checks += tails();
+      ++seg;
+    }
+    if (lane == 0 && seg > 0) mbar_drain(b_o_final, (seg - 1) & 1, a.wait_limit_ns);  // before TMEM is released
+  };
+  // ------------------------------------------------ softmax
+  auto softmax = [&] {
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    bool ok = true;
+    int seg = 0, n0 = 0, checks = 0;
+    while (ok && list.next(a, kRows, sg)) {
+      const bool valid = r < sg.rows;
+      const bool active = (warp & 3) * 32 < sg.rows;  // some row of the warp
+      int tok = 0;
+      const size_t at = valid ? row_at(a, sg, r, &tok) : 0;
+      float mul = a.scale_log2;
+      {  // this row of Q into the swizzled operand; the last segment's MMAs are done with it
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at * D);
+        float f = 1.f;
+        if constexpr (E4M3) {
+          uint32_t amax = 0;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) amax = max(amax, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
+          }
+          const int shift = f16_shift(amax);
+          f = pow2(shift);
+          mul *= pow2(-shift);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 u = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          if constexpr (E4M3) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+          }
+          sts128(sbase + C::kOffQ + (c >> 3) * C::kQPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4), w[0], w[1], w[2],
+                 w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_q_full);
+      }
+      const uint64_t bits = valid ? bits_of(a, sg.s, tok) : 0;
+      const int first_tail = tail0();
+      float m_ref = neg_inf(), l_sum = 0.f;
+      for (int j = 0; j < sg.nt; ++j) {
+        const int n = n0 + j, sb = n & 1;
+        if (!__all_sync(kFull, mbar_wait(b_s_full(sb), (n >> 1) & 1, abort_flag, a.wait_limit_ns))) {
+          if (lane == 0) give_up(46);
+          ok = false;
+          break;
+        }
+        if (!active) {
+          if (lane == 0) mbar_arrive(b_p_full(sb));
+          continue;
+        }
+        tc_fence_after();
+        uint32_t x[kPage];
+        tmem_ld_row<kPage>(tS(sb) + lane_off, x);
+        tmem_wait_ld();
+        if constexpr (E4M3) {  // the keys' scales
+          const uint32_t ks = sbase + C::kOffKScale + (n & 3) * (kPage * 4);
+#pragma unroll
+          for (int c = 0; c < kPage; c += 4) {
+            const uint4 k4 = lds128(ks + c * 4);
+            x[c] = __float_as_uint(__uint_as_float(x[c]) * __uint_as_float(k4.x));
+            x[c + 1] = __float_as_uint(__uint_as_float(x[c + 1]) * __uint_as_float(k4.y));
+            x[c + 2] = __float_as_uint(__uint_as_float(x[c + 2]) * __uint_as_float(k4.z));
+            x[c + 3] = __float_as_uint(__uint_as_float(x[c + 3]) * __uint_as_float(k4.w));
+          }
+        }
+        uint64_t bad = 0;
+        if (j >= first_tail) {
+          // which of the 64 keys this row sees
+          const int key0 = (sg.t0 + j) * kPage;
+          const int n_prefix = min(max(sg.s.prefix - key0, 0), kPage), n_len = min(sg.s.len - key0, kPage);
+          uint64_t sees = n_prefix >= 64 ? ~0ull : (1ull << n_prefix) - 1;
+          const int first = key0 - sg.s.prefix;  // drafted index of the tile's first key
+          sees |= first >= 64 ? 0 : first >= 0 ? bits >> first : first > -64 ? bits << -first : 0;
+          if (n_len < 64) sees &= (1ull << n_len) - 1;
+#pragma unroll
+          for (int c = 0; c < kPage; ++c)
+            if (!((sees >> c) & 1)) x[c] = 0xff800000u;
+          const int c = checks + j - first_tail;
+          if (!__all_sync(kFull, mbar_wait(b_checked(c), (c / kChecks) & 1, abort_flag, a.wait_limit_ns))) {
+            if (lane == 0) give_up(47);
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int w = 0; w < C::kPrep; ++w)
+            bad |= *reinterpret_cast<volatile unsigned long long*>(&misc->bad[c % kChecks][w]);
+          bad &= sees;
+        }
+        float mt = neg_inf();
+#pragma unroll
+        for (int c = 0; c < kPage; c += 2) mt = fmax3(mt, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        mt *= mul;
+        const bool moved = mt > m_ref + kRefSlack;
+        float alpha = 1.f;
+        if (moved) {
+          alpha = ex2(m_ref - mt);  // m_ref = -inf gives 0
+          m_ref = mt;
+        }
+        const float base = m_ref == neg_inf() ? 0.f : m_ref - (E4M3 ? kPShift : 0);
+        if (__any_sync(kFull, moved && j > 0)) {
+          // O is read and written back: the last P V must have finished
+          if (!__all_sync(kFull, mbar_wait(b_pv_done, (n - 1) & 1, abort_flag, a.wait_limit_ns))) {
+            if (lane == 0) give_up(48);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(tO + lane_off + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tmem_st16(tO + lane_off + c0, o);
+          }
+        }
+        // P = 2^(x - ref) over the scores: as bf16, the sum adding the rounded
+        // values; as fp16, whose rounding (2^-12) is below what cancels there
+        float rs = 0.f;
+        const bool f16 = E4M3 && f16_tile(n);
+#pragma unroll
+        for (int c0 = 0; c0 < kPage; c0 += 32) {
+          uint32_t pk[16];
+          if (f16) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float p0 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c]), mul, -base));
+              const float p1 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c + 1]), mul, -base));
+              rs += p0 + p1;
+              pk[c] = pack_f16x2(p0, p1);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float p0 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c]), mul, -base));
+              const float p1 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c + 1]), mul, -base));
+              const uint32_t w = pack_bf16x2(p0, p1);
+              rs += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
+              pk[c] = w;
+            }
+          }
+          if (bad) {  // a value that is not finite was taken out of V: NaN for whoever sees it
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              if ((bad >> (c0 + 2 * c)) & 1) pk[c] = (pk[c] & 0xffff0000u) | 0x7fc0u;
+              if ((bad >> (c0 + 2 * c + 1)) & 1) pk[c] = (pk[c] & 0xffffu) | 0x7fc00000u;
+            }
+          }
+          tmem_st16(tS(sb) + lane_off + c0 / 2, pk);
+        }
+        l_sum = l_sum * alpha + rs;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p_full(sb));
+      }
+      // ---- O / l.  Every warp waits here: Q is free for the next segment then.
+      if (!ok) break;
+      ok = __all_sync(kFull, mbar_wait(b_o_final, seg & 1, abort_flag, a.wait_limit_ns) && !*abort_flag);
+      if (!ok) break;
+      if (active) {
+        tc_fence_after();
+        const bool empty = l_sum == 0.f;  // a row that sees nothing here
+        const float inv = empty ? 0.f : 1.f / l_sum;
+        const size_t share = share_at(a, kRows, blockIdx.y, blockIdx.x, sg.place, r);
+        if (valid && !sg.whole) a.lse[share] = empty ? neg_inf() : m_ref + __log2f(l_sum) - (E4M3 ? kPShift : 0);
+        float* part = a.part + share * D;
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + at * D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t o[16];
+          tmem_ld16(tO + lane_off + c0, o);
+          tmem_wait_ld();
+          if (!valid) continue;
+          float f[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) f[c] = empty ? 0.f : __uint_as_float(o[c]) * inv;
+          if (sg.whole) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 8)
+              *reinterpret_cast<uint4*>(orow + c0 + c) =
+                  make_uint4(pack_bf16x2(f[c], f[c + 1]), pack_bf16x2(f[c + 2], f[c + 3]),
+                             pack_bf16x2(f[c + 4], f[c + 5]), pack_bf16x2(f[c + 6], f[c + 7]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; c += 4)
+              *reinterpret_cast<float4*>(part + c0 + c) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
+          }
+        }
+        tc_fence_before();  // the next segment's first P V overwrites O
+      }
+      n0 += sg.nt;
+      checks += tails();
+      ++seg;
+    }
+  };
+  // ------------------------------------------------ tiles
+  auto tiles = [&] {
+    constexpr int kN = C::kPrep * 32;
+    const int t = (threadIdx.x - C::kPrepWarp * 32) % kN, w = (warp - C::kPrepWarp) % C::kPrep;
+    bool ok = true;
+    int n0 = 0, item0 = 0, checks = 0;
+    while (ok && list.next(a, kRows, sg)) {
+      const int first_tail = tail0();
+      if constexpr (E4M3) {
+        const int is_v = warp >= C::kPrepWarp + C::kPrep ? 1 : 0;
+        for (int j = 0; j < sg.nt; ++j) {
+          const int n = n0 + j, i = item0 + (is_v ? item_v(j, sg.nt) : item_k(j)), s = i % C::kRing;
+          // The operand is free first: then the MMAs of the tiles before are
+          // issued, so the slot's last item (of the other warps, perhaps) is
+          // used up and b_full cannot be a phase behind.
+          bool got = n == 0 || mbar_wait(b_free(is_v), (n - 1) & 1, abort_flag, a.wait_limit_ns);
+          if (got) got = mbar_wait(b_full(s), (i / C::kRing) & 1, abort_flag, a.wait_limit_ns);
+          if (!__all_sync(kFull, got)) {
+            ok = false;
+            break;
+          }
+          const uint32_t src = sbase + C::kOffRing + s * C::kSlot;
+          const uint32_t scales = sbase + C::kOffScale + s * C::kScaleBytes, v_scales = scales + kPage * 4;
+          const uint32_t dst = sbase + C::kOffConv + is_v * C::kTile;
+          const bool zero = misc->bad_page[s] != 0;
+          // A thread takes 16-code chunks, eight neighbours the same chunk of
+          // eight keys: with both tiles swizzled no read or write meets a bank twice.
+          constexpr int kChunks = D / 16;
+          const bool check = is_v && j >= first_tail;
+          uint32_t bad0 = 0, bad1 = 0;  // keys 0-31 and 32-63
+          auto place = [&](int m, int& key, int& c) {
+            const int x = m * kN + t;
+            c = (x >> 3) % kChunks;
+            key = (x & 7) | (x / (8 * kChunks)) << 3;
+          };
+          auto load = [&](int key, int c) {
+            return lds128(src + key * D + ((D == 128 ? c ^ (key & 7) : c ^ ((key >> 1) & 3)) << 4));
+          };
+          auto store = [&](int key, int c, const uint32_t (&o)[8]) {
+            const uint32_t row = dst + (c >> 2) * C::kTilePanel + key * 128;
+            const int c2 = 2 * (c & 3);
+            sts128(row + ((c2 ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
+            sts128(row + (((c2 + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
+          };
+          if (!is_v) {
+            if (t < kPage) {  // for softmax, which meets the scores after the tile's slot is free again
+              const float ks = zero ? 0.f : lds_f32(scales + t * 4);
+              reinterpret_cast<float*>(smem + C::kOffKScale)[(n & 3) * kPage + t] = ks;
+              const bool fits = __all_sync(kFull, zero || fits_f16(lds_f32(v_scales + t * 4)));
+              if (lane == 0) misc->f16[n & 3][w] = fits ? 1 : 0;
+            }
+#pragma unroll
+            for (int m = 0; m < kPage * kChunks / kN; ++m) {
+              int key, c;
+              place(m, key, c);
+              const uint4 u = load(key, c);
+              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(x[e], o[2 * e], o[2 * e + 1]);
+              store(key, c, o);
+            }
+          } else {
+            const int key0 = (sg.t0 + j) * kPage;
+            const bool f16 = __all_sync(kFull, zero || (fits_f16(lds_f32(v_scales + lane * 4)) &&
+                                                        fits_f16(lds_f32(v_scales + (lane + 32) * 4))));
+            if (f16) {
+#pragma unroll
+              for (int m = 0; m < kPage * kChunks / kN; ++m) {
+                int key, c;
+                place(m, key, c);
+                uint4 u = load(key, c);
+                const float sc = zero ? 0.f : lds_f32(v_scales + key * 4);
+                if (check && key0 + key >= sg.s.len) u = make_uint4(0, 0, 0, 0);
+                const uint32_t s2 = pack_f16x2(sc, sc), x[4] = {u.x, u.y, u.z, u.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  e4m3x4_to_f16(x[e], o[2 * e], o[2 * e + 1]);
+                  o[2 * e] = mul_f16x2(o[2 * e], s2);
+                  o[2 * e + 1] = mul_f16x2(o[2 * e + 1], s2);
+                }
+                store(key, c, o);
+              }
+            } else {
+#pragma unroll 1
+              for (int m = 0; m < kPage * kChunks / kN; ++m) {
+                int key, c;
+                place(m, key, c);
+                const uint4 u = load(key, c);
+                const float sc = lds_f32(v_scales + key * 4);
+                const uint32_t s2 = pack_bf16x2(sc, sc), x[4] = {u.x, u.y, u.z, u.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  o[2 * e] = mul_bf16x2(e4m3_hi_to_bf16x2(__byte_perm(x[e], 0, 0x1000)), s2);
+                  o[2 * e + 1] = mul_bf16x2(e4m3_hi_to_bf16x2(__byte_perm(x[e], 0, 0x3020)), s2);
+                }
+                if (check) {
+                  bool clear = key0 + key >= sg.s.len;
+                  bool nf = false;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) nf |= has_nonfinite(o[e]);
+                  if (nf && !clear && key0 + key >= sg.s.prefix) {
+                    (key < 32 ? bad0 : bad1) |= 1u << (key & 31);
+                    clear = true;
+                  }
+                  if (clear) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = 0;
+                  }
+                }
+                store(key, c, o);
+              }
+            }
+          }
+          if (check) {
+            bad0 = __reduce_or_sync(kFull, bad0);
+            bad1 = __reduce_or_sync(kFull, bad1);
+          }
+          const int c = checks + j - first_tail;
+          if (check && lane == 0) misc->bad[c % kChecks][w] = static_cast<unsigned long long>(bad1) << 32 | bad0;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(b_empty(s));
+            mbar_arrive(b_ready(is_v));
+            if (check) mbar_arrive(b_checked(c));
+          }
+        }
+      } else {
+        // V tiles that hold drafted keys: slots past the end are cleared, and
+        // values that are not finite taken out (softmax makes up for them)
+        for (int j = first_tail; j < sg.nt; ++j) {
+          const int c = checks + j - first_tail;
+          if (!__all_sync(kFull, mbar_wait(b_drafted(c), (c / kChecks) & 1, abort_flag, a.wait_limit_ns))) {
+            ok = false;
+            break;
+          }
+          const uint32_t tile = sbase + C::kOffRing + ((item0 + item_v(j, sg.nt)) % C::kRing) * C::kSlot;
+          const int key0 = (sg.t0 + j) * kPage;
+          unsigned long long bad = 0;
+          for (int base = 0; base < kPage * (D / 8); base += kN) {
+            const int chunk = base + t, key = (chunk / 8) % kPage;  // panels of [64][128 B]
+            const uint32_t at = tile + chunk * 16;  // the swizzle stays inside a row
+            const uint4 u = lds128(at);
+            const bool past = key0 + key >= sg.s.len;
+            const bool nf = !past && key0 + key >= sg.s.prefix &&
+                            (has_nonfinite(u.x) || has_nonfinite(u.y) || has_nonfinite(u.z) || has_nonfinite(u.w));
+            if (past || nf) sts128(at, 0, 0, 0, 0);
+            const unsigned vote = __ballot_sync(kFull, nf);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if ((vote >> (8 * y)) & 0xff) bad |= 1ull << (((base + w * 32) / 8 + y) % kPage);
+          }
+          if (lane == 0) misc->bad[c % kChecks][w] = bad;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_checked(c));
+        }
+      }
+      n0 += sg.nt;
+      item0 += 2 * sg.nt;
+      checks += tails();
+    }
+    if (!ok && lane == 0) give_up(49);
+  };
+
+  if (warp < 4) {
+    if constexpr (E4M3) reg_dec<C::kRegsIssue>();
+    if (warp == 0)
+      copies();
+    else if (warp == 1)
+      issue();
+    else if constexpr (!E4M3)
+      tiles();
+  } else if (warp < 8) {
+    if constexpr (E4M3) reg_inc<C::kRegsSoftmax>();
+    softmax();
+  } else if constexpr (E4M3) {
+    reg_dec<C::kRegsPrep>();
+    tiles();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tO, C::kTmemCols);
+  }
+}
+
+template <int D, bool E4M3>
+int launch_t(const TreeLaunch& a) {
+  using C = Cfg<D, E4M3>;
+  auto kern = tree_rows128_kernel<D, E4M3>;
+  static uint64_t attr_done = 0;  // one bit per device ordinal
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return ATTN_ERR_CUDA;
+  if (!(attr_done >> dev & 1)) {
+    if (E4M3) {  // a warpgroup that asked for more registers than the launch left would wait for good
+      static_assert(C::kRegsIssue + C::kRegsSoftmax + 2 * C::kRegsPrep <= 4 * C::kRegs, "register split");
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return ATTN_ERR_CUDA;
+      if (fa.numRegs != C::kRegs) return ATTN_ERR_UNSUPPORTED;
+    }
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    attr_done |= uint64_t(1) << dev;
+  }
+  CUtensorMap mk, mv;
+  const int groups = a.num_pages * a.Hkv;
+  if (E4M3 ? !tma_map_codes(&mk, a.K, groups, D) || !tma_map_codes(&mv, a.V, groups, D)
+           : !tma_map_bhnd(&mk, a.K, groups, kPage, D, kPage) || !tma_map_bhnd(&mv, a.V, groups, kPage, D, kPage))
+    return ATTN_ERR_CUDA;
+  kern<<<dim3(a.ctas, a.planes), C::kThreads, C::kSmem, a.stream>>>(mk, mv, a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_tree_rows128(const TreeLaunch& a) {
+  if (a.d == 64) return a.k_scales ? launch_t<64, true>(a) : launch_t<64, false>(a);
+  return a.k_scales ? launch_t<128, true>(a) : launch_t<128, false>(a);
+}
+
+}  // namespace bss
