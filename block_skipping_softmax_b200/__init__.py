@@ -177,8 +177,11 @@ def attn_decode_noalloc(q, K, V, o, B, Hq, Hkv, L, d, tau, stream=None, skip_mas
     return lib().attn_decode_noalloc(q, K, V, o, B, Hq, Hkv, L, d, float(tau), stream, skip_mask)
 
 
+_STRIDES = {n: ctypes.c_longlong * n for n in (6, 12)}
+
+
 def _strides(values):
-    return (ctypes.c_longlong * len(values))(*values)
+    return _STRIDES[len(values)](*values)
 
 
 def attn_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, B, N, Hq, Hkv, d, rot_dim,
@@ -502,61 +505,81 @@ def decode_paged(q, K_pages, V_pages, block_table, seq_lens, max_seq_len: int, t
     return (o, mask) if skip_mask else o
 
 
-# ---- cache and tree helpers ---------------------------------------------------
+# ---- rotation, cache and tree helpers -----------------------------------------
+#
+# These run once a layer and token, beside kernels of a few microseconds: checks
+# are plain comparisons, and messages are made only when one fails.
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise AttnError(1, what)
+def _no(what: str, why: str) -> AttnError:
+    return AttnError(1, f"{what} ({why})")
 
 
-def _on_current_device(what: str, *tensors):
-    """Every tensor is on the current CUDA device (the library launches there)."""
+def _device(what, tensors) -> int:
+    """The index of the tensors' one device, which is the current one (the library launches there)."""
     import torch
 
+    dev = tensors[0].get_device()
     for t in tensors:
-        _need(t is None or t.is_cuda, f"{what} (tensors must be CUDA tensors)")
-    dev = torch.cuda.current_device()
+        if t is not None and t.get_device() != dev:
+            raise _no(what, "tensors must be on one CUDA device")
+    if dev < 0:
+        raise _no(what, "tensors must be CUDA tensors")
+    if dev != torch.cuda.current_device():
+        raise _no(what, "tensors must be on the current CUDA device")
+    return dev
+
+
+def _raw_stream(dev: int) -> int:
+    """The current stream's cudaStream_t, without making a Stream object."""
+    import torch
+
+    try:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    except AttributeError:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _run(dev, stream, tensors, make, call):
+    """call(make(), raw stream) on `stream` (None: the current one).  Memory that
+    make() allocates belongs to that stream, and tensors that meet it from
+    another one are recorded on it, so that the caching allocator keeps them
+    until the call's kernels are done."""
+    import torch
+
+    if stream is None or stream.cuda_stream == _raw_stream(dev):
+        new = make()
+        return new, call(new, _raw_stream(dev))
     for t in tensors:
-        _need(t is None or t.device.index == dev, f"{what} (tensors must be on the current CUDA device)")
+        if t is not None:
+            t.record_stream(stream)
+    current = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        new = make()
+    for t in new:
+        if t is not None:
+            t.record_stream(current)
+            t.record_stream(stream)
+    return new, call(new, stream.cuda_stream)
 
 
-class _Launch:
-    """The stream of one call.  Memory that the call allocates belongs to that
-    stream; tensors that meet it from another one are recorded on it, so that
-    the caching allocator keeps them until the call's kernels are done."""
+def _contiguous_like(x):
+    import torch
 
-    def __init__(self, stream, *tensors):
-        import torch
-
-        self.current = torch.cuda.current_stream()
-        self.stream = self.current if stream is None else stream
-        self.other = self.stream.cuda_stream != self.current.cuda_stream
-        if self.other:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-
-    def empty(self, shape, dtype, device):
-        import torch
-
-        if not self.other:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=device)
-        t.record_stream(self.current)
-        return t
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
-def _token_layout(x):
-    """(B, N, H, d, strides) of [tokens, H, d] or [B, H, N, d] with contiguous d;
-    strides of axes of length 1 count as 0."""
+def _token_strides(what, x):
+    """(batch, token, head) strides of [tokens, H, d] or [B, H, N, d]; an axis of length 1 counts as 0."""
     if x.dim() == 3:
-        (N, H, d), (sn, sh, sd) = x.shape, x.stride()
-        B, sb = 1, 0
+        (N, H, _), (sn, sh, sd) = x.shape, x.stride()
+        sb = 0
     else:
-        (B, H, N, d), (sb, sh, sn, sd) = x.shape, x.stride()
-    _need(sd == 1, "tensors need contiguous heads")
-    return B, N, H, d, (sb if B > 1 else 0, sn if N > 1 else 0, sh if H > 1 else 0)
+        (B, H, N, _), (sb, sh, sn, sd) = x.shape, x.stride()
+        if B == 1:
+            sb = 0
+    if sd != 1:
+        raise _no(what, "the d elements of a head must be contiguous")
+    return sb, sn if N > 1 else 0, sh if H > 1 else 0
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -574,60 +597,76 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     import torch
 
     what = "qk_norm_rope"
-    _need(q.dim() in (3, 4) and k.dim() == q.dim(), f"{what} (q and k must be [tokens, H, d] or [B, H, N, d])")
-    B, N, Hq, d, sq = _token_layout(q)
-    Bk, Nk, Hkv, dk, sk = _token_layout(k)
-    _need((B, N, d) == (Bk, Nk, dk), f"{what} (q and k must have the same tokens and head size)")
-    _need(q.dtype == torch.bfloat16 and k.dtype == torch.bfloat16, f"{what} (q and k must be bf16)")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    pos_stride = 0
-    if rot:
-        _need(inv_freq.dtype == torch.float32 and inv_freq.is_contiguous(), f"{what} (inv_freq must be float32)")
-        shapes = ((N,), (B, N)) if q.dim() == 4 else ((N,),)
-        _need(positions.dtype == torch.int32 and positions.shape in shapes and
-              (N == 1 or positions.stride(-1) == 1), f"{what} (positions must be int32 [N] or [B, N])")
-        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    for w in (q_weight, k_weight):
-        _need(w is None or (w.dtype == torch.bfloat16 and w.shape == (d,) and (w.is_contiguous())),
-              f"{what} (weights must be bf16 [d])")
-    _on_current_device(what, q, k, q_weight, k_weight, *((positions, inv_freq) if rot else ()))
-    run = _Launch(stream, q, k, positions, inv_freq, q_weight, k_weight, *(out or ()))
-    if out is None:
-        qo, ko = (run.empty(x.shape, x.dtype, x.device) for x in (q, k))
+    bf16 = torch.bfloat16
+    if q.dim() not in (3, 4) or k.dim() != q.dim():
+        raise _no(what, "q and k must be [tokens, H, d] or [B, H, N, d]")
+    if q.dim() == 3:
+        (N, Hq, d), (Nk, Hkv, dk), B, Bk = q.shape, k.shape, 1, 1
     else:
-        qo, ko = out
-        for x, y in ((q, qo), (k, ko)):
-            _need(y.shape == x.shape and y.dtype == torch.bfloat16, f"{what} (out must be bf16 of the inputs' shapes)")
-        _on_current_device(what, qo, ko)
-    so, sp = _token_layout(qo)[4], _token_layout(ko)[4]
-    st = attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(),
-                           positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None,
-                           None if q_weight is None else q_weight.data_ptr(),
-                           None if k_weight is None else k_weight.data_ptr(), B, N, Hq, Hkv, d, rot, interleaved,
-                           eps, sq + sk + so + sp, pos_stride, run.stream.cuda_stream)
-    _check(st, "attn_qk_norm_rope")
-    return qo, ko
+        (B, Hq, N, d), (Bk, Hkv, Nk, dk) = q.shape, k.shape
+    if N != Nk or d != dk or B != Bk:
+        raise _no(what, "q and k must have the same tokens and head size")
+    if q.dtype is not bf16 or k.dtype is not bf16:
+        raise _no(what, "q and k must be bf16")
+    rot = pos_stride = 0
+    pos_ptr = freq_ptr = None
+    tensors = [q, k]
+    if inv_freq is not None and inv_freq.numel():
+        if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous():
+            raise _no(what, "inv_freq must be contiguous float32")
+        shape = positions.shape
+        if (positions.dtype is not torch.int32 or (N > 1 and positions.stride(-1) != 1) or
+                not (shape == (N,) or (q.dim() == 4 and shape == (B, N)))):
+            raise _no(what, "positions must be int32 [N] or [B, N]")
+        if len(shape) == 2 and B > 1:
+            pos_stride = positions.stride(0)
+        rot, pos_ptr, freq_ptr = 2 * inv_freq.numel(), positions.data_ptr(), inv_freq.data_ptr()
+        tensors += (positions, inv_freq)
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if w.dtype is not bf16 or w.shape != (d,) or not w.is_contiguous():
+                raise _no(what, "weights must be contiguous bf16 [d]")
+            tensors.append(w)
+    if out is not None:
+        if out[0].shape != q.shape or out[1].shape != k.shape or out[0].dtype is not bf16 or out[1].dtype is not bf16:
+            raise _no(what, "out must be bf16 of the inputs' shapes")
+        tensors += out
+    strides = _token_strides(what, q) + _token_strides(what, k)
+    out_strides = None if out is None else _token_strides(what, out[0]) + _token_strides(what, out[1])
+    dev = _device(what, tensors)
+
+    def call(new, raw):
+        qo, ko = new
+        so = out_strides or _token_strides(what, qo) + _token_strides(what, ko)
+        return lib().attn_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(), pos_ptr, freq_ptr,
+            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+            B, N, Hq, Hkv, d, rot, interleaved, eps, _strides(strides + so), pos_stride, raw)
+
+    new, st = _run(dev, stream, tensors,
+                   lambda: out if out is not None else (_contiguous_like(q), _contiguous_like(k)), call)
+    if st:
+        raise AttnError(st, "attn_qk_norm_rope")
+    return new
 
 
 def _check_codes(what, K_codes, V_codes, K_scales, V_scales):
     import torch
 
-    _need(K_codes.dim() == 4 and K_codes.shape[2] == attn_decode_tile(),
-          f"{what} (codes must be [num_pages, Hkv, 64, d])")
-    for c in (K_codes, V_codes):
-        _need(c.dtype == torch.uint8 and c.shape == K_codes.shape and c.is_contiguous(),
-              f"{what} (codes must be contiguous uint8 of one shape)")
-    for s in (K_scales, V_scales):
-        _need(s.dtype == torch.float32 and s.shape == K_codes.shape[:3] and s.is_contiguous(),
-              f"{what} (scales must be contiguous float32 [num_pages, Hkv, 64])")
+    shape = K_codes.shape
+    if len(shape) != 4 or shape[2] != 64 or V_codes.shape != shape or K_codes.dtype is not torch.uint8 or \
+            V_codes.dtype is not torch.uint8 or not K_codes.is_contiguous() or not V_codes.is_contiguous():
+        raise _no(what, "codes must be contiguous uint8 [num_pages, Hkv, 64, d]")
+    if K_scales.shape != shape[:3] or V_scales.shape != shape[:3] or K_scales.dtype is not torch.float32 or \
+            V_scales.dtype is not torch.float32 or not K_scales.is_contiguous() or not V_scales.is_contiguous():
+        raise _no(what, "scales must be contiguous float32 [num_pages, Hkv, 64]")
 
 
-def _check_slots(what, slots, B, N, packed):
+def _check_slots(what, slots):
     import torch
 
-    shape = (N,) if packed else (B, N)
-    _need(slots.dtype == torch.int64 and slots.shape == shape and slots.is_contiguous(),
-          f"{what} (slots must be contiguous int64, one for each token)")
+    if slots.dtype is not torch.int64 or slots.dim() not in (1, 2) or not slots.is_contiguous():
+        raise _no(what, "slots must be contiguous int64, [tokens] or [B, N]")
 
 
 def cache_write_e4m3(k, v, slots, K_codes, V_codes, K_scales, V_scales, stream=None) -> None:
@@ -642,20 +681,30 @@ def cache_write_e4m3(k, v, slots, K_codes, V_codes, K_scales, V_scales, stream=N
     import torch
 
     what = "cache_write_e4m3"
-    _need(k.dim() in (3, 4) and k.shape == v.shape, f"{what} (k and v must be [tokens, H, d] or [B, H, N, d])")
-    _need(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16, f"{what} (k and v must be bf16)")
-    B, N, Hkv, d, sk = _token_layout(k)
-    sv = _token_layout(v)[4]
+    if k.dim() not in (3, 4) or k.shape != v.shape:
+        raise _no(what, "k and v must be [tokens, H, d] or [B, H, N, d], of one shape")
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
+        raise _no(what, "k and v must be bf16")
     _check_codes(what, K_codes, V_codes, K_scales, V_scales)
-    _need(K_codes.shape[1] == Hkv and K_codes.shape[3] == d, f"{what} (the pool has other heads than k)")
-    _check_slots(what, slots, B, N, k.dim() == 3)
-    every = (k, v, slots, K_codes, V_codes, K_scales, V_scales)
-    _on_current_device(what, *every)
-    run = _Launch(stream, *every)
-    st = attn_cache_write_e4m3(k.data_ptr(), v.data_ptr(), slots.data_ptr(), K_codes.data_ptr(),
-                               V_codes.data_ptr(), K_scales.data_ptr(), V_scales.data_ptr(), B, N, Hkv,
-                               K_codes.shape[0], d, sk + sv, run.stream.cuda_stream)
-    _check(st, "attn_cache_write_e4m3")
+    _check_slots(what, slots)
+    if k.dim() == 3:
+        (N, Hkv, d), B, tokens = k.shape, 1, k.shape[:1]
+    else:
+        B, Hkv, N, d = k.shape
+        tokens = (B, N)
+    pages, pool_heads, _, pool_d = K_codes.shape
+    if pool_heads != Hkv or pool_d != d:
+        raise _no(what, "the pool has other heads than k")
+    if slots.shape != tokens:
+        raise _no(what, "slots must have one entry a token")
+    tensors = (k, v, slots, K_codes, V_codes, K_scales, V_scales)
+    dev = _device(what, tensors)
+    strides = _strides(_token_strides(what, k) + _token_strides(what, v))
+    _, st = _run(dev, stream, tensors, tuple, lambda _, raw: lib().attn_cache_write_e4m3(
+        k.data_ptr(), v.data_ptr(), slots.data_ptr(), K_codes.data_ptr(), V_codes.data_ptr(), K_scales.data_ptr(),
+        V_scales.data_ptr(), B, N, Hkv, pages, d, strides, raw))
+    if st:
+        raise AttnError(st, "attn_cache_write_e4m3")
 
 
 def cache_read_e4m3(K_codes, V_codes, K_scales, V_scales, slots, out=None, stream=None):
@@ -668,28 +717,35 @@ def cache_read_e4m3(K_codes, V_codes, K_scales, V_scales, slots, out=None, strea
     import torch
 
     what = "cache_read_e4m3"
+    bf16 = torch.bfloat16
     _check_codes(what, K_codes, V_codes, K_scales, V_scales)
+    _check_slots(what, slots)
     pages, Hkv, _, d = K_codes.shape
-    _need(slots.dim() in (1, 2), f"{what} (slots must be [tokens] or [B, N])")
-    shape = (slots.shape[0], Hkv, d) if slots.dim() == 1 else (slots.shape[0], Hkv, slots.shape[1], d)
-    every = (K_codes, V_codes, K_scales, V_scales, slots)
-    _on_current_device(what, *every)
-    run = _Launch(stream, *every, *(out or ()))
-    if out is None:
-        k, v = (run.empty(shape, torch.bfloat16, slots.device) for _ in range(2))
+    if slots.dim() == 1:
+        N, B = slots.shape[0], 1
+        shape = (N, Hkv, d)
     else:
-        k, v = out
-        for t in (k, v):
-            _need(t.shape == shape and t.dtype == torch.bfloat16, f"{what} (out must be bf16 of shape {shape})")
-        _on_current_device(what, k, v)
-    B, N, _, _, sk = _token_layout(k)
-    sv = _token_layout(v)[4]
-    _check_slots(what, slots, B, N, slots.dim() == 1)
-    st = attn_cache_read_e4m3(K_codes.data_ptr(), V_codes.data_ptr(), K_scales.data_ptr(), V_scales.data_ptr(),
-                              slots.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, Hkv, pages, d, sk + sv,
-                              run.stream.cuda_stream)
-    _check(st, "attn_cache_read_e4m3")
-    return k, v
+        B, N = slots.shape
+        shape = (B, Hkv, N, d)
+    tensors = (K_codes, V_codes, K_scales, V_scales, slots)
+    if out is not None:
+        for t in out:
+            if t.shape != shape or t.dtype is not bf16:
+                raise _no(what, "out must be bf16, [tokens, Hkv, d] or [B, Hkv, N, d] as slots are")
+        tensors += tuple(out)
+        _token_strides(what, out[0]), _token_strides(what, out[1])
+    dev = _device(what, tensors)
+
+    def make():
+        return out if out is not None else (K_scales.new_empty(shape, dtype=bf16), K_scales.new_empty(shape, dtype=bf16))
+
+    new, st = _run(dev, stream, tensors, make, lambda new, raw: lib().attn_cache_read_e4m3(
+        K_codes.data_ptr(), V_codes.data_ptr(), K_scales.data_ptr(), V_scales.data_ptr(), slots.data_ptr(),
+        new[0].data_ptr(), new[1].data_ptr(), B, N, Hkv, pages, d,
+        _strides(_token_strides(what, new[0]) + _token_strides(what, new[1])), raw))
+    if st:
+        raise AttnError(st, "attn_cache_read_e4m3")
+    return new
 
 
 def tree_paged(q, K_pages, V_pages, block_table, seq_lens, cu_q, max_q: int, max_seq_len: int, tree_mask=None,
@@ -707,9 +763,9 @@ def tree_paged(q, K_pages, V_pages, block_table, seq_lens, cu_q, max_q: int, max
     """
     import torch
 
-    for t in (K_pages, V_pages):
-        _need(t.dtype == torch.bfloat16 and t.is_contiguous() and t.shape == K_pages.shape,
-              "tree_paged (pages must be contiguous bf16 of one shape)")
+    if K_pages.dtype is not torch.bfloat16 or V_pages.dtype is not torch.bfloat16 or V_pages.shape != K_pages.shape or \
+            not K_pages.is_contiguous() or not V_pages.is_contiguous():
+        raise _no("tree_paged", "pages must be contiguous bf16 of one shape")
     return _tree("tree_paged", q, K_pages, V_pages, None, None, block_table, seq_lens, cu_q, max_q, max_seq_len,
                  tree_mask, out, stream, workspace)
 
@@ -726,40 +782,58 @@ def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
           stream, workspace):
     import torch
 
-    _need(q.dim() == 3 and q.dtype == torch.bfloat16 and q.is_contiguous(),
-          f"{what} (q must be contiguous bf16 [total_q, Hq, d])")
+    bf16, int32 = torch.bfloat16, torch.int32
+    if q.dim() != 3 or q.dtype is not bf16 or not q.is_contiguous():
+        raise _no(what, "q must be contiguous bf16 [total_q, Hq, d]")
     total, Hq, d = q.shape
-    _need(K.dim() == 4 and K.shape[2] == attn_decode_tile() and K.shape[3] == d,
-          f"{what} (the cache must be [num_pages, Hkv, 64, d])")
-    pages, Hkv = K.shape[0], K.shape[1]
-    for t in (block_table, seq_lens, cu_q):
-        _need(t.dtype == torch.int32 and t.is_contiguous(),
-              f"{what} (block_table, seq_lens and cu_q must be contiguous int32)")
+    if K.dim() != 4 or K.shape[2] != 64 or K.shape[3] != d:
+        raise _no(what, "the cache must be [num_pages, Hkv, 64, d]")
+    pages, Hkv = K.shape[:2]
+    if block_table.dtype is not int32 or seq_lens.dtype is not int32 or cu_q.dtype is not int32 or \
+            not block_table.is_contiguous() or not seq_lens.is_contiguous() or not cu_q.is_contiguous():
+        raise _no(what, "block_table, seq_lens and cu_q must be contiguous int32")
     B = seq_lens.numel()
-    _need(block_table.dim() == 2 and block_table.shape[0] == B and cu_q.numel() == B + 1,
-          f"{what} (block_table must be [B, max_pages] and cu_q [B + 1])")
+    if block_table.dim() != 2 or block_table.shape[0] != B or cu_q.numel() != B + 1:
+        raise _no(what, "block_table must be [B, max_pages] and cu_q [B + 1]")
+    tensors = [q, K, V, block_table, seq_lens, cu_q]
+    if K_scales is not None:
+        tensors += (K_scales, V_scales)
     if tree_mask is not None:
-        _need(tree_mask.dtype == torch.int64 and tree_mask.shape == (total,) and tree_mask.is_contiguous(),
-              f"{what} (tree_mask must be contiguous int64 [total_q])")
-    every = (q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, tree_mask, out, workspace)
-    _on_current_device(what, *every)
-    run = _Launch(stream, *every)
-    o = run.empty(q.shape, q.dtype, q.device) if out is None else out
+        if tree_mask.dtype is not torch.int64 or tree_mask.shape != (total,) or not tree_mask.is_contiguous():
+            raise _no(what, "tree_mask must be contiguous int64 [total_q]")
+        tensors.append(tree_mask)
     if out is not None:
-        _need(o.shape == q.shape and o.dtype == torch.bfloat16 and o.is_contiguous(),
-              f"{what} (out must be contiguous bf16 of q's shape)")
-    ws = workspace
-    if ws is None:
-        need = attn_tree_workspace_bytes(B, max_q, total, Hq, Hkv, max_seq_len, d)
-        ws = run.empty((need,), torch.uint8, q.device) if need else None
-    mask = None if tree_mask is None else tree_mask.data_ptr()
-    ws_ptr, ws_bytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
-    tail = (block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), mask, o.data_ptr(), B, max_q, total, Hq,
-            Hkv, pages, block_table.shape[1], max_seq_len, d, run.stream.cuda_stream, ws_ptr, ws_bytes)
-    if K_scales is None:
-        st = attn_tree_paged(q.data_ptr(), K.data_ptr(), V.data_ptr(), *tail)
+        if out.shape != q.shape or out.dtype is not bf16 or not out.is_contiguous():
+            raise _no(what, "out must be contiguous bf16 of q's shape")
+        tensors.append(out)
+    need = 0
+    if workspace is not None:
+        if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+            raise _no(what, "workspace must be contiguous uint8")
+        tensors.append(workspace)
     else:
-        st = attn_tree_paged_e4m3(q.data_ptr(), K.data_ptr(), V.data_ptr(), K_scales.data_ptr(),
-                                  V_scales.data_ptr(), *tail)
-    _check(st, "attn_" + what)
-    return o
+        need = lib().attn_tree_workspace_bytes(B, max_q, total, Hq, Hkv, max_seq_len, d)
+    dev = _device(what, tensors)
+
+    def make():
+        return (torch.empty_like(q) if out is None else out,
+                seq_lens.new_empty((need,), dtype=torch.uint8) if need else workspace)
+
+    def call(new, raw):
+        o, ws = new
+        mask = None if tree_mask is None else tree_mask.data_ptr()
+        ws_ptr, ws_bytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+        if K_scales is None:
+            return lib().attn_tree_paged(
+                q.data_ptr(), K.data_ptr(), V.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
+                mask, o.data_ptr(), B, max_q, total, Hq, Hkv, pages, block_table.shape[1], max_seq_len, d, raw, ws_ptr,
+                ws_bytes)
+        return lib().attn_tree_paged_e4m3(
+            q.data_ptr(), K.data_ptr(), V.data_ptr(), K_scales.data_ptr(), V_scales.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), cu_q.data_ptr(), mask, o.data_ptr(), B, max_q, total, Hq, Hkv, pages,
+            block_table.shape[1], max_seq_len, d, raw, ws_ptr, ws_bytes)
+
+    new, st = _run(dev, stream, tensors, make, call)
+    if st:
+        raise AttnError(st, "attn_" + what)
+    return new[0]

@@ -36,35 +36,31 @@ struct CacheArgs {
   float* scales[2];
   const long long* slots;
   long long xs[2][3];  // strides in elements: batch, token, head
-  long long rows;      // B * N * 2 * Hkv
   long long n_slots;   // num_pages * 64
-  int N, Hkv;
+  int B, N, Hkv;
 };
 
-// Row = one head's key or value vector of one token; the 2 Hkv rows of a token
-// are neighbours, keys first.
+// A CTA takes neighbouring tokens of one head's keys or values, which are
+// neighbours in [B, H, N, d] and in a page; the CTAs of a token's other heads
+// run beside it, which are neighbours in a packed [tokens, H, d].
 struct Row {
   bool valid;
-  int side, h;
-  long long x_at;     // element offset in x[side]
-  long long slot;     // -1 where the token has none
-  long long code_at;  // vector index in codes[side] / scales[side]
+  long long x_at;  // element offset in x[side]
+  long long at;    // vector index in codes[side] and scales[side], -1 where the token has no slot
 };
 
-__device__ __forceinline__ Row row_of(const CacheArgs& a, long long r) {
+__device__ __forceinline__ Row row_of(const CacheArgs& a, unsigned t, int side, int h) {
   Row w;
-  w.valid = r < a.rows;
-  const unsigned per = 2u * a.Hkv;
-  const unsigned t = w.valid ? static_cast<unsigned>(r / per) : 0u;  // token: B * N < 2^31
-  const unsigned hh = w.valid ? static_cast<unsigned>(r - static_cast<long long>(t) * per) : 0u;
-  w.side = hh >= static_cast<unsigned>(a.Hkv);
-  w.h = hh - (w.side ? a.Hkv : 0);
-  const unsigned b = t / a.N, n = t % a.N;
-  w.x_at = w.side ? b * a.xs[1][0] + n * a.xs[1][1] + w.h * a.xs[1][2]
-                  : b * a.xs[0][0] + n * a.xs[0][1] + w.h * a.xs[0][2];
-  w.slot = w.valid ? a.slots[t] : -1;
-  if (w.slot < 0 || w.slot >= a.n_slots) w.slot = -1;
-  w.code_at = w.slot < 0 ? 0 : ((w.slot / kPage) * a.Hkv + w.h) * kPage + w.slot % kPage;
+  w.valid = t < static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N);  // B * N < 2^31
+  w.x_at = 0;
+  w.at = -1;
+  if (w.valid) {
+    const unsigned b = a.B == 1 ? 0 : t / a.N, n = t - b * a.N;
+    const long long slot = a.slots[t];
+    w.x_at = side ? b * a.xs[1][0] + n * a.xs[1][1] + h * a.xs[1][2]
+                  : b * a.xs[0][0] + n * a.xs[0][1] + h * a.xs[0][2];
+    if (slot >= 0 && slot < a.n_slots) w.at = ((slot / kPage) * a.Hkv + h) * kPage + slot % kPage;
+  }
   return w;
 }
 
@@ -73,15 +69,18 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kThreads / kLanes;
   const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  const unsigned block = blockIdx.x / (2u * a.Hkv), head = blockIdx.x - block * (2u * a.Hkv);
+  const int side = head >= static_cast<unsigned>(a.Hkv), h = side ? head - a.Hkv : head;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(side ? a.x[1] : a.x[0]);
+  uint8_t* codes = side ? a.codes[1] : a.codes[0];
+  float* scales = side ? a.scales[1] : a.scales[0];
   Row row[R];
   uint4 u[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    row[r] = row_of(a, (static_cast<long long>(blockIdx.x) * R + r) * kGroups + group);
+    row[r] = row_of(a, (block * R + r) * kGroups + group, side, h);
     u[r] = make_uint4(0, 0, 0, 0);
-    if (row[r].slot >= 0)
-      u[r] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>((row[r].side ? a.x[1] : a.x[0])) +
-                                             row[r].x_at + c * 8);
+    if (row[r].at >= 0) u[r] = *reinterpret_cast<const uint4*>(x + row[r].x_at + c * 8);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -115,10 +114,9 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a
             "f"(__uint_as_float(w[2 * i + 1] << 16) * inv));
       out[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
     }
-    if (row[r].slot >= 0) {
-      *reinterpret_cast<uint2*>((row[r].side ? a.codes[1] : a.codes[0]) + row[r].code_at * D + c * 8) =
-          make_uint2(out[0], out[1]);
-      if (c == 0) (row[r].side ? a.scales[1] : a.scales[0])[row[r].code_at] = s;
+    if (row[r].at >= 0) {
+      *reinterpret_cast<uint2*>(codes + row[r].at * D + c * 8) = make_uint2(out[0], out[1]);
+      if (c == 0) scales[row[r].at] = s;
     }
   }
 }
@@ -128,17 +126,22 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a)
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kThreads / kLanes;
   const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  const unsigned block = blockIdx.x / (2u * a.Hkv), head = blockIdx.x - block * (2u * a.Hkv);
+  const int side = head >= static_cast<unsigned>(a.Hkv), h = side ? head - a.Hkv : head;
+  __nv_bfloat16* x = static_cast<__nv_bfloat16*>(const_cast<void*>(side ? a.x[1] : a.x[0]));
+  const uint8_t* codes = side ? a.codes[1] : a.codes[0];
+  const float* scales = side ? a.scales[1] : a.scales[0];
   Row row[R];
   uint2 u[R];
   float s[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    row[r] = row_of(a, (static_cast<long long>(blockIdx.x) * R + r) * kGroups + group);
+    row[r] = row_of(a, (block * R + r) * kGroups + group, side, h);
     u[r] = make_uint2(0, 0);
     s[r] = 0.f;
-    if (row[r].slot >= 0) {
-      u[r] = *reinterpret_cast<const uint2*>((row[r].side ? a.codes[1] : a.codes[0]) + row[r].code_at * D + c * 8);
-      s[r] = (row[r].side ? a.scales[1] : a.scales[0])[row[r].code_at];
+    if (row[r].at >= 0) {
+      u[r] = *reinterpret_cast<const uint2*>(codes + row[r].at * D + c * 8);
+      s[r] = scales[row[r].at];
     }
   }
 #pragma unroll
@@ -153,16 +156,15 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a)
       out[i] = pack_bf16x2(__low2float(h) * s[r], __high2float(h) * s[r]);
     }
     if (row[r].valid)
-      *reinterpret_cast<uint4*>(
-          const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>((row[r].side ? a.x[1] : a.x[0]))) +
-          row[r].x_at + c * 8) = make_uint4(out[0], out[1], out[2], out[3]);
+      *reinterpret_cast<uint4*>(x + row[r].x_at + c * 8) = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
 template <int D, bool WRITE, int R>
 int launch_r(const CacheArgs& a, cudaStream_t s) {
   constexpr int kGroups = kThreads / (D / 8);
-  const long long grid = (a.rows + kGroups * R - 1) / (kGroups * R);
+  const long long tokens = static_cast<long long>(a.B) * a.N;
+  const long long grid = (tokens + kGroups * R - 1) / (kGroups * R) * 2 * a.Hkv;
   if (grid > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   if constexpr (WRITE)
     cache_write_kernel<D, R><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
@@ -175,7 +177,8 @@ int launch_r(const CacheArgs& a, cudaStream_t s) {
 template <int D, bool WRITE>
 int launch_d(const CacheArgs& a, cudaStream_t s) {
   constexpr int kGroups = kThreads / (D / 8);
-  if (a.rows <= 148LL * 4 * kGroups) return launch_r<D, WRITE, 1>(a, s);
+  const long long rows = static_cast<long long>(a.B) * a.N * 2 * a.Hkv;
+  if (rows <= 148LL * 4 * kGroups) return launch_r<D, WRITE, 1>(a, s);
   return launch_r<D, WRITE, 4>(a, s);
 }
 
@@ -207,7 +210,7 @@ int run(const void* k, const void* v, const int64_t* slots, const void* K_codes,
   a.slots = reinterpret_cast<const long long*>(slots);
   for (int t = 0; t < 2; ++t)
     for (int i = 0; i < 3; ++i) a.xs[t][i] = strides[3 * t + i];
-  a.rows = static_cast<long long>(B) * N * 2 * Hkv;
+  a.B = B;
   a.n_slots = static_cast<long long>(num_pages) * kPage;
   a.N = N;
   a.Hkv = Hkv;

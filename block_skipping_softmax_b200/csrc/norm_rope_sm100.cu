@@ -11,10 +11,13 @@
 // position 2^17 an fp32 product is already off by 2^-8 rad.
 //
 // Bound by HBM: every element is read once and written once.  A row (one head
-// of one token) is held by D/8 lanes of 16 bytes, so the mean is a 3- or
-// 4-step butterfly and a pair (i, i + rot/2) one shuffle.  A CTA takes the
-// heads of one token, which share the angles: rot/2 threads compute sines and
-// cosines once into shared memory while the rows' loads are in flight.
+// of one token) is held by D/16 lanes with two chunks of 8 elements each, the
+// two that meet in the rotation, so a pair needs no shuffle and the mean a
+// butterfly of 2 or 3 steps.  A CTA takes several tokens; `groups` groups of
+// lanes share a token's heads, so that a thread stays with one token and one
+// chunk of its angles, and loads a row ahead of the one that it turns.  The
+// tokens' sines and cosines are made once, into shared memory, while the first
+// rows are on their way.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,7 +42,9 @@ struct RopeArgs {
   const float* inv_freq;
   long long xs[2][3], ys[2][3];  // strides in elements: batch, token, head
   long long pos_stride_b;
-  int N, Hq, H, rot, interleaved;  // H = Hq + Hkv
+  int B, N, Hq, H, rot, interleaved;  // H = Hq + Hkv
+  int groups;  // groups of lanes that share a token
+  int heads;   // of a token in a CTA
   float eps;
 };
 
@@ -52,124 +57,142 @@ __device__ __forceinline__ void unpack8(const uint4 u, float (&f)[8]) {
   }
 }
 
-// R rows for each group of D/8 lanes, all loaded before the angles are known.
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs a) {
-  constexpr int kLanes = D / 8;               // lanes of a row
+// CTA (x, y): kGroups / groups tokens, their heads [y * heads, ...).
+template <int D, bool NORM>
+__global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kLanes = D / 16;              // lanes of a row
   constexpr int kGroups = kThreads / kLanes;  // rows at a time
-  __shared__ __align__(16) float s_cos[D / 2], s_sin[D / 2];
-  const int b = blockIdx.x / a.N, n = blockIdx.x % a.N;
-  const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes;  // c: chunk of 8 elements
-  const int head0 = blockIdx.y * (kGroups * R) + group;
-
-  uint4 u[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int h = head0 + r * kGroups;
-    const int side = h >= a.Hq;
-    u[r] = make_uint4(0, 0, 0, 0);
-    if (h < a.H)
-      u[r] = *reinterpret_cast<const uint4*>(a.x[side] + b * a.xs[side][0] + n * a.xs[side][1] +
-                                             (h - (side ? a.Hq : 0)) * a.xs[side][2] + c * 8);
-  }
+  extern __shared__ __align__(16) float s_angle[];  // [token][cos, sin][rot / 2]
+  const int group = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
   const int half = a.rot / 2;
-  if (threadIdx.x < half) {
-    const double turns = static_cast<double>(a.pos[b * a.pos_stride_b + n]) *
-                         static_cast<double>(a.inv_freq[threadIdx.x]) * 0.15915494309189533577;
-    const float part = static_cast<float>(turns - rint(turns));  // a turn: [-1/2, 1/2]
-    sincospif(2.f * part, &s_sin[threadIdx.x], &s_cos[threadIdx.x]);
+  // this lane's chunks: i and i + rot/16 of the rotated part, or two beyond it
+  const bool turned = l * 8 < half;
+  const int c0 = turned ? l * 8 : 16 * l, step = turned ? half : 8;
+  const int T = kGroups / a.groups, token = group / a.groups;
+  const unsigned tokens = static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N);
+  const unsigned tok0 = blockIdx.x * T, t = tok0 + token;
+  const bool live = t < tokens;
+  long long xq = 0, xk = 0, yq = 0, yk = 0;
+  if (live) {
+    const unsigned b = a.B == 1 ? 0 : t / a.N, n = t - b * a.N;
+    xq = b * a.xs[0][0] + n * a.xs[0][1] + c0;
+    xk = b * a.xs[1][0] + n * a.xs[1][1] + c0 - a.Hq * a.xs[1][2];
+    yq = b * a.ys[0][0] + n * a.ys[0][1] + c0;
+    yk = b * a.ys[1][0] + n * a.ys[1][1] + c0 - a.Hq * a.ys[1][2];
+  }
+  const int end = min(a.H, static_cast<int>(blockIdx.y + 1) * a.heads);
+  int h = blockIdx.y * a.heads + group - token * a.groups;
+  uint4 u[2];
+  auto load = [&](int head) {
+    u[0] = u[1] = make_uint4(0, 0, 0, 0);
+    if (live && head < end) {
+      const __nv_bfloat16* x = head < a.Hq ? a.x[0] + xq + head * a.xs[0][2] : a.x[1] + xk + head * a.xs[1][2];
+      u[0] = *reinterpret_cast<const uint4*>(x);
+      u[1] = *reinterpret_cast<const uint4*>(x + step);
+    }
+  };
+  load(h);
+  for (int i = threadIdx.x; i < T * half; i += kThreads) {
+    const unsigned ti = i / half, f = i - ti * half, tt = tok0 + ti;
+    if (tt < tokens) {
+      const unsigned b = a.B == 1 ? 0 : tt / a.N, n = tt - b * a.N;
+      const double turns = static_cast<double>(a.pos[b * a.pos_stride_b + n]) * static_cast<double>(a.inv_freq[f]) *
+                           0.15915494309189533577;
+      const float part = static_cast<float>(turns - rint(turns));  // of a turn: [-1/2, 1/2]
+      sincospif(2.f * part, &s_angle[ti * a.rot + half + f], &s_angle[ti * a.rot + f]);
+    }
   }
   __syncthreads();
+  // interleaved: the pairs lie inside a chunk, 4 angles each
+  const float* angle = s_angle + token * a.rot + (a.interleaved ? c0 / 2 : c0);
 
-  // this chunk's angles: 4 pairs inside the chunk, or 8 pairs with the chunk
-  // rot/16 chunks away (the first half takes -sin, the second half +sin)
-  const bool turned = c * 8 < a.rot;
-  const bool second = c * 8 >= half;
-  float cs[8], sn[8];
-  int partner = threadIdx.x & 31;
-  if (turned && a.interleaved) {
+  // every lane of a warp makes every round: the shuffles are warp-wide
+  for (int round = blockIdx.y * a.heads; round < end; round += a.groups, h += a.groups) {
+    float f[2][8];
+    unpack8(u[0], f[0]);
+    unpack8(u[1], f[1]);
+    load(h + a.groups);
+    const bool key = h >= a.Hq;
+    if constexpr (NORM) {
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      cs[2 * i] = cs[2 * i + 1] = s_cos[c * 4 + i];
-      sn[2 * i + 1] = s_sin[c * 4 + i];
-      sn[2 * i] = -sn[2 * i + 1];
+      for (int i = 0; i < 8; ++i) ss = fmaf(f[0][i], f[0][i], fmaf(f[1][i], f[1][i], ss));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+      const __nv_bfloat16* w = key ? a.w[1] : a.w[0];
+      if (w) {
+        const float rs = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float wf[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w + c0 + x * step)), wf);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[x][i] *= rs * wf[i];
+        }
+      }
     }
-  } else if (turned) {
-    const int at = second ? c * 8 - half : c * 8;
+    if (turned) {  // an element outside the rotated part stays as it is, NaN and inf among them
+      if (a.interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cs[i] = s_cos[at + i];
-      sn[i] = second ? s_sin[at + i] : -s_sin[at + i];
+        for (int x = 0; x < 2; ++x) {
+          const float4 c4 = *reinterpret_cast<const float4*>(angle + x * step / 2);
+          const float4 s4 = *reinterpret_cast<const float4*>(angle + half + x * step / 2);
+          const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = f[x][2 * i], q = f[x][2 * i + 1];
+            f[x][2 * i] = fmaf(p, cs[i], -q * sn[i]);
+            f[x][2 * i + 1] = fmaf(q, cs[i], p * sn[i]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 c4 = *reinterpret_cast<const float4*>(angle + i);
+          const float4 s4 = *reinterpret_cast<const float4*>(angle + half + i);
+          const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = f[0][i + e], q = f[1][i + e];
+            f[0][i + e] = fmaf(p, cs[e], -q * sn[e]);
+            f[1][i + e] = fmaf(q, cs[e], p * sn[e]);
+          }
+        }
+      }
     }
-    partner += second ? -(half / 8) : half / 8;
-  } else {
+    if (live && h < end) {
+      __nv_bfloat16* y = key ? a.y[1] + yk + h * a.ys[1][2] : a.y[0] + yq + h * a.ys[0][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+      for (int x = 0; x < 2; ++x)
+        *reinterpret_cast<uint4*>(y + x * step) =
+            make_uint4(pack_bf16x2(f[x][0], f[x][1]), pack_bf16x2(f[x][2], f[x][3]), pack_bf16x2(f[x][4], f[x][5]),
+                       pack_bf16x2(f[x][6], f[x][7]));
+    }
   }
-
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int h = head0 + r * kGroups;
-    const int side = h >= a.Hq;
-    float f[8];
-    unpack8(u[r], f);
-    const __nv_bfloat16* w = a.w[side];
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-    if (w) {
-      const float rs = rsqrtf(ss * (1.f / D) + a.eps);
-      float wf[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + c), wf);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= rs * wf[i];
-    }
-    float g[8];
-    if (a.interleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = f[i ^ 1];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = __shfl_sync(kFull, f[i], partner);
-    }
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // an element outside the rotated part stays as it is, NaN and inf among them
-      const float lo = turned ? fmaf(f[2 * i], cs[2 * i], g[2 * i] * sn[2 * i]) : f[2 * i];
-      const float hi =
-          turned ? fmaf(f[2 * i + 1], cs[2 * i + 1], g[2 * i + 1] * sn[2 * i + 1]) : f[2 * i + 1];
-      o[i] = pack_bf16x2(lo, hi);
-    }
-    if (h < a.H)
-      *reinterpret_cast<uint4*>(a.y[side] + b * a.ys[side][0] + n * a.ys[side][1] +
-                                (h - (side ? a.Hq : 0)) * a.ys[side][2] + c * 8) =
-          make_uint4(o[0], o[1], o[2], o[3]);
-  }
-}
-
-template <int D, int R>
-void launch_r(const RopeArgs& a, unsigned tokens, int ny, cudaStream_t s) {
-  norm_rope_kernel<D, R><<<dim3(tokens, ny), kThreads, 0, s>>>(a);
 }
 
 template <int D>
-void launch_d(const RopeArgs& a, unsigned tokens, cudaStream_t s) {
-  constexpr int kGroups = kThreads / (D / 8);
-  const int passes = (a.H + kGroups - 1) / kGroups;
-  // Rows of a group: one where the whole launch fits the 148 SMs at once (the
-  // latency of a call is then one row's), else up to four, so that a CTA's
-  // loads cover the memory latency and its angles serve more heads.
-  int ny = passes;
-  if (static_cast<long long>(tokens) * passes > 148 * 4) ny = (passes + 3) / 4;
-  switch ((a.H + kGroups * ny - 1) / (kGroups * ny)) {
-    case 1: return launch_r<D, 1>(a, tokens, ny, s);
-    case 2: return launch_r<D, 2>(a, tokens, ny, s);
-    case 3: return launch_r<D, 3>(a, tokens, ny, s);
-    default: return launch_r<D, 4>(a, tokens, ny, s);
+void launch_d(RopeArgs& a, cudaStream_t s) {
+  constexpr int kGroups = kThreads / (D / 16);
+  const unsigned tokens = static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N);
+  const unsigned passes = (a.H + kGroups - 1) / kGroups;
+  a.groups = kGroups;
+  a.heads = a.H;
+  if (static_cast<long long>(tokens) * passes <= 148 * 6) {
+    // all rows at once: the latency of a call is one row's
+    a.heads = kGroups;
+  } else {
+    // the most groups a token that leave at most a tenth of them idle
+    auto idle = [&](int g) { return 10 * (((a.H + g - 1) / g) * g - a.H) > ((a.H + g - 1) / g) * g; };
+    while (a.groups > 1 && idle(a.groups)) a.groups /= 2;
   }
+  const int T = kGroups / a.groups;
+  const dim3 grid((tokens + T - 1) / T, (a.H + a.heads - 1) / a.heads);
+  const size_t smem = static_cast<size_t>(T) * a.rot * sizeof(float);
+  if (a.w[0] || a.w[1])
+    norm_rope_kernel<D, true><<<grid, kThreads, smem, s>>>(a);
+  else
+    norm_rope_kernel<D, false><<<grid, kThreads, smem, s>>>(a);
 }
 
 }  // namespace
@@ -220,11 +243,11 @@ extern "C" int attn_qk_norm_rope(const void* q, const void* k, void* q_out, void
   a.rot = rot_dim;
   a.interleaved = interleaved ? 1 : 0;
   a.eps = eps;
-  const unsigned tokens = static_cast<unsigned>(B) * static_cast<unsigned>(N);
+  a.B = B;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
-    launch_d<64>(a, tokens, s);
+    launch_d<64>(a, s);
   else
-    launch_d<128>(a, tokens, s);
+    launch_d<128>(a, s);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
