@@ -106,8 +106,10 @@ struct TreeLaunch {
   cudaStream_t stream;
 };
 
-int launch_tree_rows16(const TreeLaunch& a);   // tree_rows16_sm100.cu
-int launch_tree_rows128(const TreeLaunch& a);  // tree_rows128_sm100.cu
+// rows of a CTA: 8, 16 or 32 (tree_few_sm100.cu), with so many CTAs an SM
+int launch_tree_few(const TreeLaunch& a, int rows);
+int tree_few_ctas(int rows);
+int launch_tree_many(const TreeLaunch& a);  // 128 rows, 2 CTAs an SM (tree_many_sm100.cu)
 
 // Current device (sm_100 checked) and its device status word (api.cu).
 int device_context(int* dev, int** status);

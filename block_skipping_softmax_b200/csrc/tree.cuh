@@ -12,8 +12,7 @@
 namespace bss {
 
 constexpr int kPage = kDecodeTile;  // 64 keys: one page, one tile
-constexpr int kFewRows = 16;        // rows of a CTA of the two kernels
-constexpr int kManyRows = 128;
+constexpr int kManyRows = 128;      // rows of a CTA of the tcgen05 kernel
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kRefSlack = 8.f;  // log2 units: the reference maximum lags by less, so p < 2^8
 
@@ -240,9 +239,9 @@ __device__ __forceinline__ uint64_t bits_of(const TreeLaunch& a, const Seq& s, i
   return a.mask ? a.mask[s.tok0 + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
 }
 
-// Tensor map over a pool of e4m3 codes [groups, 64, D], d fastest: boxes of a
-// whole group (64 keys), rows swizzled as 128 bytes (D = 128) or 64 (D = 64);
-// groups past the end read as zeros.
-bool tma_map_codes(CUtensorMap* m, const void* base, long long groups, int D);
+// Tensor map over a pool of e4m3 codes [groups, 64, D], d fastest: boxes of
+// `keys` keys, rows swizzled as 128 bytes (D = 128) or 64 (D = 64); groups past
+// the end read as zeros.
+bool tma_map_codes(CUtensorMap* m, const void* base, long long groups, int D, int keys);
 
 }  // namespace bss

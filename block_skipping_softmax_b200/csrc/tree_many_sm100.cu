@@ -91,7 +91,7 @@ __device__ __forceinline__ bool item_is_v(int i, int nt, int& tile) {
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
-    tree_rows128_kernel(const __grid_constant__ CUtensorMap tmK,
+    tree_many_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeLaunch a) {
   using C = Cfg<D, E4M3>;
   static_assert(sizeof(Misc) <= C::kMiscBytes && C::kRing <= 8 && C::kPrep <= 4, "misc layout");
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
 template <int D, bool E4M3>
 int launch_t(const TreeLaunch& a) {
   using C = Cfg<D, E4M3>;
-  auto kern = tree_rows128_kernel<D, E4M3>;
+  auto kern = tree_many_kernel<D, E4M3>;
   static uint64_t attr_done = 0;  // one bit per device ordinal
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return ATTN_ERR_CUDA;
@@ -710,7 +710,7 @@ int launch_t(const TreeLaunch& a) {
   }
   CUtensorMap mk, mv;
   const int groups = a.num_pages * a.Hkv;
-  if (E4M3 ? !tma_map_codes(&mk, a.K, groups, D) || !tma_map_codes(&mv, a.V, groups, D)
+  if (E4M3 ? !tma_map_codes(&mk, a.K, groups, D, kPage) || !tma_map_codes(&mv, a.V, groups, D, kPage)
            : !tma_map_bhnd(&mk, a.K, groups, kPage, D, kPage) || !tma_map_bhnd(&mv, a.V, groups, kPage, D, kPage))
     return ATTN_ERR_CUDA;
   kern<<<dim3(a.ctas, a.planes), C::kThreads, C::kSmem, a.stream>>>(mk, mv, a);
@@ -719,7 +719,7 @@ int launch_t(const TreeLaunch& a) {
 
 }  // namespace
 
-int launch_tree_rows128(const TreeLaunch& a) {
+int launch_tree_many(const TreeLaunch& a) {
   if (a.d == 64) return a.k_scales ? launch_t<64, true>(a) : launch_t<64, false>(a);
   return a.k_scales ? launch_t<128, true>(a) : launch_t<128, false>(a);
 }

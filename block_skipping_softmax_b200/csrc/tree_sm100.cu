@@ -140,15 +140,15 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d) {
   Plan p{};
   const long long rows = static_cast<long long>(max_q) * (Hq / Hkv);
-  // 16 rows where all rows of a KV head fit (a decode of single tokens with up
-  // to 16 query heads a group), else 128.
-  p.per = rows <= kFewRows ? kFewRows : kManyRows;
+  // The least number of rows a CTA that holds all rows of a KV head, up to 32:
+  // the warp-level MMAs' time grows with the rows.  Beyond, 128 on tcgen05.
+  p.per = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kManyRows;
   p.planes = static_cast<int>((rows + p.per - 1) / p.per);
   const long long tiles = (L + kPage - 1) / kPage;
   p.min_tiles = 4;
-  // 148 SMs x 2 CTAs
+  const long long slots = 148 * (p.per < kManyRows ? tree_few_ctas(p.per) : 2);
   const long long most = (tiles * B * Hkv + p.min_tiles - 1) / p.min_tiles;
-  const long long fit = p.planes < 296 ? 296 / p.planes : 1;
+  const long long fit = p.planes < slots ? slots / p.planes : 1;
   p.ctas = static_cast<int>(most < fit ? most : fit);
   p.shares = tiles > 1 && p.ctas > 1;
   if (p.shares) {
@@ -195,7 +195,7 @@ int run_tree(TreeLaunch& a, void* ws, size_t ws_bytes, void* stream) {
   a.wait_limit_ns = wait_limit_ns();
   a.scale_log2 = 1.4426950408889634f / std::sqrt(static_cast<float>(a.d));
   a.stream = static_cast<cudaStream_t>(stream);
-  st = p.per == kFewRows ? launch_tree_rows16(a) : launch_tree_rows128(a);
+  st = p.per < kManyRows ? launch_tree_few(a, p.per) : launch_tree_many(a);
   if (st != ATTN_OK || !p.shares) return st;
   // four warps a row where a KV head has many shares
   const bool many = p.ctas > 8ll * a.B * a.Hkv;
@@ -205,7 +205,7 @@ int run_tree(TreeLaunch& a, void* ws, size_t ws_bytes, void* stream) {
 
 }  // namespace
 
-bool tma_map_codes(CUtensorMap* m, const void* base, long long groups, int D) {
+bool tma_map_codes(CUtensorMap* m, const void* base, long long groups, int D, int keys) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     cudaDriverEntryPointQueryResult q;
@@ -217,7 +217,7 @@ bool tma_map_codes(CUtensorMap* m, const void* base, long long groups, int D) {
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(kPage), static_cast<cuuint64_t>(groups)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(kPage) * D};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(kPage), 1};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(keys), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
