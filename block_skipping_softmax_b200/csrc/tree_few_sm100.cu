@@ -39,14 +39,14 @@ struct Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kCtas = NT == 4 ? 2 : 3;                // of an SM
   static constexpr int kRowBytes = E4M3 ? D : 2 * D;
-  static constexpr int kKB = kRowBytes == 256 ? 1 : 2;         // blocks of 16 keys that a warp takes of a page
+  static constexpr int kKB = kRowBytes == 256 || (kRowBytes == 128 && E4M3 && NT == 4) ? 1 : 2;         // blocks of 16 keys that a warp takes of a page
   static constexpr int kKeys = 16 * kKB;
   static constexpr int kShare = kPage / kKeys;                 // warps that share a page
   static constexpr int kEvery = kWarps / kShare;               // a warp takes every kEvery-th page
   static constexpr int kTile = kKeys * kRowBytes;              // a warp's keys (or values) of a page
   static constexpr int kPanels = E4M3 ? 1 : D / 64;            // swizzled panels of it
   static constexpr int kScaleBytes = E4M3 ? kKeys * 4 : 0;
-  static constexpr int kStages = kRowBytes == 64 ? 4 : 2;
+  static constexpr int kStages = (kRowBytes == 64 ? 4 : 2) * (kKB == 1 && kRowBytes != 256 ? 2 : 1);
   static constexpr int kStageBytes = 2 * kTile;
   static constexpr int kOffScale = kWarps * kStages * kStageBytes;  // [warp][stage][K, V][keys] floats
   static constexpr int kOffRed = kOffScale + kWarps * kStages * 2 * kScaleBytes;  // rows x D floats
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, E4M3, NT>::kCtas)
 
     for (int i = 0; i < mine && ok; ++i) {
       const int s = slot;
-      ok = __all_sync(kFull, mbar_wait(bars + 8 * s, phase, abort_flag, a.wait_limit_ns));
+      ok = __all_sync(kFull, mbar_poll(bars + 8 * s, phase, abort_flag, a.wait_limit_ns));
       if (!ok) {
         if (lane == 0) {
           *abort_flag = 1;

@@ -48,7 +48,7 @@ struct Cfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffConv = kOffQ + kRows * D * 2;           // e4m3: K and V operands
   static constexpr int kOffRing = kOffConv + (E4M3 ? 2 * kTile : 0);
-  static constexpr int kScaleBytes = E4M3 ? 2 * kPage * 4 : 0;    // K (a K tile's slot only), V
+  static constexpr int kScaleBytes = E4M3 ? 2 * kPage * 4 : 0;    // K, V
   static constexpr int kOffScale = kOffRing + kRing * kSlot;       // e4m3: [slot][K, V][64] floats
   static constexpr int kOffKScale = kOffScale + kRing * kScaleBytes;  // e4m3: [4][64], for softmax
   static constexpr int kOffBar = kOffKScale + (E4M3 ? 4 * kPage * 4 : 0);
@@ -67,7 +67,7 @@ struct Misc {
   uint32_t tmem_base;
   int abort;
   int bad_page[8];  // e4m3: the slot's page id was out of range
-  int f16[4][2];    // e4m3, by tile: whether V (keys 0-31, 32-63) is an fp16 operand
+  int plain[4][2];  // e4m3, by tile: whether the scales of keys 0-31, 32-63 fit fp16 operands
 };
 
 // kind::f16 with fp16 A and B (format 0), fp32 accumulation, A K-major
@@ -158,9 +158,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
     *abort_flag = 1;
     atomicCAS(a.status, 0, ATTN_DEVICE_TIMEOUT_BASE + site);
   };
-  // e4m3: V of tile n is an fp16 operand (known once K of tile n is ready)
-  auto f16_tile = [&](int n) {
-    const volatile int* f = misc->f16[n & 3];
+  // e4m3: K and V of tile n are fp16 operands with their scales in them (known
+  // once K of tile n is ready).  Else K holds the codes alone, whose scales
+  // softmax applies, and V and P are bf16.
+  auto plain_tile = [&](int n) {
+    const volatile int* f = misc->plain[n & 3];
     return (f[0] & f[1]) != 0;
   };
   // Tiles from tail0 on hold drafted keys or end past the last key; there are at
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
         const int s = issued % C::kRing;
         if (lane == 0) {
           if (issued >= C::kRing)
-            ok = mbar_wait(b_empty(s), ((issued / C::kRing) - 1) & 1, abort_flag, a.wait_limit_ns);
+            ok = mbar_poll(b_empty(s), ((issued / C::kRing) - 1) & 1, abort_flag, a.wait_limit_ns);
           if (ok) {
             const bool good = page >= 0 && page < a.num_pages;
             const long long grp = static_cast<long long>(good ? page : a.num_pages) * a.Hkv + sg.kv;
@@ -198,12 +200,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
             // a page id out of range reads zeros: the box lies past the pool's end
             if constexpr (E4M3) {
               misc->bad_page[s] = good ? 0 : 1;
-              mbar_arrive_expect_tx(b_full(s), C::kRaw + (good ? (is_v ? 1 : 2) * kPage * 4 : 0));
+              mbar_arrive_expect_tx(b_full(s), C::kRaw + (good ? C::kScaleBytes : 0));
               tma_load_3d(dst, is_v ? &tmV : &tmK, b_full(s), 0, 0, static_cast<int>(grp));
               if (good) {
-                // the value scales come with K too, for the choice of P's type
+                // both with both, for the choice of the operands' type
                 const uint32_t to = sbase + C::kOffScale + s * C::kScaleBytes;
-                if (!is_v) bulk_load(to, a.k_scales + grp * kPage, kPage * 4, b_full(s));
+                bulk_load(to, a.k_scales + grp * kPage, kPage * 4, b_full(s));
                 bulk_load(to + kPage * 4, a.v_scales + grp * kPage, kPage * 4, b_full(s));
               }
             } else {
@@ -239,55 +241,61 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
     constexpr uint32_t idS = E4M3 ? idesc_f16_f32(kRows, kPage, false) : idesc_bf16_f32(kRows, kPage, false, false);
     constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true), idPV16 = idesc_f16_f32(kRows, D, true);
     auto wait = [&](uint32_t bar, int parity, int site) {
-      if (mbar_wait(bar, parity, abort_flag, a.wait_limit_ns)) return true;
+      if (mbar_poll(bar, parity, abort_flag, a.wait_limit_ns)) return true;
       give_up(site);
       return false;
     };
+    // descriptors: the high words are constants, an MMA adds offsets to the low ones
+    constexpr uint32_t hi = sw128_desc_hi(1024);
+    const uint32_t dQ = sw128_desc_lo(sbase + C::kOffQ, 16);
+    const uint32_t dK = sw128_desc_lo(sbase + (E4M3 ? C::kOffConv : C::kOffRing), 16);
+    const uint32_t dV = sw128_desc_lo(sbase + (E4M3 ? C::kOffConv + C::kTile : C::kOffRing), C::kTilePanel);
     bool ok = true;
-    int seg = 0, n0 = 0, item0 = 0, checks = 0;  // segments, tiles, ring items and drafted tiles before this one
+    int seg = 0, n0 = 0, checks = 0;  // segments, tiles and drafted tiles before this one
+    int slot = 0, phase = 0;          // bf16: the ring's items are used in its order
     while (ok && list.next(a, kRows, sg)) {
       if (lane == 0) {
         const int nt = sg.nt, first_tail = tail0();
         ok = wait(b_q_full, seg & 1, 41);
         for (int j = 0; ok && nt > 0 && j <= nt; ++j) {
           if (j < nt) {
-            const int n = n0 + j, i = item0 + item_k(j), s = i % C::kRing;
-            const uint32_t sK = sbase + (E4M3 ? C::kOffConv : C::kOffRing + s * C::kSlot);
-            if (!(ok = E4M3 ? wait(b_ready(0), n & 1, 42) : wait(b_full(s), (i / C::kRing) & 1, 42))) break;
+            const int n = n0 + j;
+            const uint32_t at = E4M3 ? dK : dK + slot * (C::kSlot >> 4);
+            if (!(ok = E4M3 ? wait(b_ready(0), n & 1, 42) : wait(b_full(slot), phase, 42))) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk & 3) * 32;  // 16 values = 32 B inside a 128 B row
-              mma_ss(tS(n & 1), sw128_desc(sbase + C::kOffQ + (kk >> 2) * C::kQPanel + off, 16, 1024),
-                     sw128_desc(sK + (kk >> 2) * C::kTilePanel + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+              constexpr int kStep = 32 >> 4;  // 16 values = 32 B inside a 128 B row
+              mma_ss(tS(n & 1), desc_join(dQ + (kk >> 2) * (C::kQPanel >> 4) + (kk & 3) * kStep, hi),
+                     desc_join(at + (kk >> 2) * (C::kTilePanel >> 4) + (kk & 3) * kStep, hi), idS, kk > 0 ? 1u : 0u);
             }
             mma_commit(b_s_full(n & 1));
-            mma_commit(E4M3 ? b_free(0) : b_empty(s));
+            mma_commit(E4M3 ? b_free(0) : b_empty(slot));
+            if (++slot == C::kRing) slot = 0, phase ^= 1;
           }
           if (j >= 1) {
-            const int t = j - 1, n = n0 + t, i = item0 + item_v(t, nt), s = i % C::kRing;
-            const uint32_t sV = sbase + (E4M3 ? C::kOffConv + C::kTile : C::kOffRing + s * C::kSlot);
-            if (!(ok = E4M3 ? wait(b_ready(1), n & 1, 43) : wait(b_full(s), (i / C::kRing) & 1, 43))) break;
+            const int t = j - 1, n = n0 + t;
+            const uint32_t at = E4M3 ? dV : dV + slot * (C::kSlot >> 4);
+            if (!(ok = E4M3 ? wait(b_ready(1), n & 1, 43) : wait(b_full(slot), phase, 43))) break;
             if (!E4M3 && t >= first_tail) {
               const int c = checks + t - first_tail;
               if (!(ok = wait(b_checked(c), (c / kChecks) & 1, 44))) break;
             }
             if (!(ok = wait(b_p_full(n & 1), (n >> 1) & 1, 45))) break;
             tc_fence_after();
-            const uint32_t id = E4M3 && f16_tile(n) ? idPV16 : idPV;
+            const uint32_t id = E4M3 && plain_tile(n) ? idPV16 : idPV;
 #pragma unroll
             for (int kk = 0; kk < kPage / 16; ++kk)
-              mma_ts(tO, tS(n & 1) + kk * 8, sw128_desc(sV + kk * 16 * 128, C::kTilePanel, 1024), id,
-                     (t > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(E4M3 ? b_free(1) : b_empty(s));
+              mma_ts(tO, tS(n & 1) + kk * 8, desc_join(at + kk * (16 * 128 >> 4), hi), id, (t > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(E4M3 ? b_free(1) : b_empty(slot));
             mma_commit(b_pv_done);
+            if (++slot == C::kRing) slot = 0, phase ^= 1;
           }
         }
         mma_commit(b_o_final);
       }
       ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
       n0 += sg.nt;
-      item0 += 2 * sg.nt;
       checks += tails();
       ++seg;
     }
@@ -342,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
       float m_ref = neg_inf(), l_sum = 0.f;
       for (int j = 0; j < sg.nt; ++j) {
         const int n = n0 + j, sb = n & 1;
-        if (!__all_sync(kFull, mbar_wait(b_s_full(sb), (n >> 1) & 1, abort_flag, a.wait_limit_ns))) {
+        if (!__all_sync(kFull, mbar_poll(b_s_full(sb), (n >> 1) & 1, abort_flag, a.wait_limit_ns))) {
           if (lane == 0) give_up(46);
           ok = false;
           break;
@@ -352,34 +360,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           continue;
         }
         tc_fence_after();
-        uint32_t x[kPage];
-        tmem_ld_row<kPage>(tS(sb) + lane_off, x);
-        tmem_wait_ld();
-        if constexpr (E4M3) {  // the keys' scales
-          const uint32_t ks = sbase + C::kOffKScale + (n & 3) * (kPage * 4);
-#pragma unroll
-          for (int c = 0; c < kPage; c += 4) {
-            const uint4 k4 = lds128(ks + c * 4);
-            x[c] = __float_as_uint(__uint_as_float(x[c]) * __uint_as_float(k4.x));
-            x[c + 1] = __float_as_uint(__uint_as_float(x[c + 1]) * __uint_as_float(k4.y));
-            x[c + 2] = __float_as_uint(__uint_as_float(x[c + 2]) * __uint_as_float(k4.z));
-            x[c + 3] = __float_as_uint(__uint_as_float(x[c + 3]) * __uint_as_float(k4.w));
-          }
-        }
-        uint64_t bad = 0;
+        // which of the 64 keys this row sees, and which of their values are not finite
+        uint64_t sees = ~0ull, bad = 0;
         if (j >= first_tail) {
-          // which of the 64 keys this row sees
           const int key0 = (sg.t0 + j) * kPage;
           const int n_prefix = min(max(sg.s.prefix - key0, 0), kPage), n_len = min(sg.s.len - key0, kPage);
-          uint64_t sees = n_prefix >= 64 ? ~0ull : (1ull << n_prefix) - 1;
+          sees = n_prefix >= 64 ? ~0ull : (1ull << n_prefix) - 1;
           const int first = key0 - sg.s.prefix;  // drafted index of the tile's first key
           sees |= first >= 64 ? 0 : first >= 0 ? bits >> first : first > -64 ? bits << -first : 0;
           if (n_len < 64) sees &= (1ull << n_len) - 1;
-#pragma unroll
-          for (int c = 0; c < kPage; ++c)
-            if (!((sees >> c) & 1)) x[c] = 0xff800000u;
           const int c = checks + j - first_tail;
-          if (!__all_sync(kFull, mbar_wait(b_checked(c), (c / kChecks) & 1, abort_flag, a.wait_limit_ns))) {
+          if (!__all_sync(kFull, mbar_poll(b_checked(c), (c / kChecks) & 1, abort_flag, a.wait_limit_ns))) {
             if (lane == 0) give_up(47);
             ok = false;
             break;
@@ -389,68 +380,134 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
             bad |= *reinterpret_cast<volatile unsigned long long*>(&misc->bad[c % kChecks][w]);
           bad &= sees;
         }
-        float mt = neg_inf();
+        const bool plain = !E4M3 || plain_tile(n);
+        // an unusual e4m3 tile: 16 columns at a time, with their scales and mask
+        auto scaled16 = [&](int c0, uint32_t (&y)[16]) {
+          tmem_ld16(tS(sb) + lane_off + c0, y);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < kPage; c += 2) mt = fmax3(mt, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        mt *= mul;
-        const bool moved = mt > m_ref + kRefSlack;
-        float alpha = 1.f;
-        if (moved) {
-          alpha = ex2(m_ref - mt);  // m_ref = -inf gives 0
-          m_ref = mt;
-        }
-        const float base = m_ref == neg_inf() ? 0.f : m_ref - (E4M3 ? kPShift : 0);
-        if (__any_sync(kFull, moved && j > 0)) {
-          // O is read and written back: the last P V must have finished
-          if (!__all_sync(kFull, mbar_wait(b_pv_done, (n - 1) & 1, abort_flag, a.wait_limit_ns))) {
-            if (lane == 0) give_up(48);
-            ok = false;
-            break;
+          for (int c = 0; c < 16; ++c) {
+            const float ks = lds_f32(sbase + C::kOffKScale + ((n & 3) * kPage + c0 + c) * 4);
+            y[c] = __float_as_uint(__uint_as_float(y[c]) * ks);
+            if (!((sees >> (c0 + c)) & 1)) y[c] = 0xff800000u;
           }
-          tc_fence_after();
+        };
+        // the tile's maximum to the running reference; moves O along, and gives
+        // the value that the exponents are relative to
+        float alpha = 1.f, base = 0.f, rs = 0.f;
+        auto refer = [&](float mt) {
+          mt *= mul;
+          const bool moved = mt > m_ref + kRefSlack;
+          if (moved) {
+            alpha = ex2(m_ref - mt);  // m_ref = -inf gives 0
+            m_ref = mt;
+          }
+          base = m_ref == neg_inf() ? 0.f : m_ref - (E4M3 ? kPShift : 0);
+          if (__any_sync(kFull, moved && j > 0)) {
+            // O is read and written back: the last P V must have finished
+            if (!__all_sync(kFull, mbar_poll(b_pv_done, (n - 1) & 1, abort_flag, a.wait_limit_ns))) {
+              if (lane == 0) give_up(48);
+              return false;
+            }
+            tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld16(tO + lane_off + c0, o);
-            tmem_wait_ld();
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + lane_off + c0, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tmem_st16(tO + lane_off + c0, o);
+              for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tmem_st16(tO + lane_off + c0, o);
+            }
           }
-        }
+          return true;
+        };
         // P = 2^(x - ref) over the scores: as bf16, the sum adding the rounded
         // values; as fp16, whose rounding (2^-12) is below what cancels there
-        float rs = 0.f;
-        const bool f16 = E4M3 && f16_tile(n);
+        if (plain) {
+          uint32_t x[kPage];
+          tmem_ld_row<kPage>(tS(sb) + lane_off, x);
+          tmem_wait_ld();
+          if (j >= first_tail) {
 #pragma unroll
-        for (int c0 = 0; c0 < kPage; c0 += 32) {
-          uint32_t pk[16];
-          if (f16) {
+            for (int c = 0; c < kPage; ++c)
+              if (!((sees >> c) & 1)) x[c] = 0xff800000u;
+          }
+          float mt[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+          for (int c = 0; c < kPage; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mt[e] = fmax3(mt[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+          if (!(ok = refer(fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]))))) break;
+          float rs2 = 0.f;
+#pragma unroll
+          for (int c0 = 0; c0 < kPage; c0 += 32) {
+            uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               const float p0 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c]), mul, -base));
               const float p1 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c + 1]), mul, -base));
-              rs += p0 + p1;
-              pk[c] = pack_f16x2(p0, p1);
+              if constexpr (E4M3) {
+                pk[c] = pack_f16x2(p0, p1);
+                rs += p0;
+                rs2 += p1;
+              } else {
+                pk[c] = pack_bf16x2(p0, p1);
+                rs += __uint_as_float(pk[c] << 16);
+                rs2 += __uint_as_float(pk[c] & 0xffff0000u);
+              }
             }
-          } else {
+            tmem_st16(tS(sb) + lane_off + c0 / 2, pk);
+          }
+          rs += rs2;
+        } else {  // an unusual e4m3 tile: 16 columns at a time, with their scales and mask
+          auto scaled16 = [&](int c0, uint32_t (&y)[16]) {
+            tmem_ld16(tS(sb) + lane_off + c0, y);
+            tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const float p0 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c]), mul, -base));
-              const float p1 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c + 1]), mul, -base));
-              const uint32_t w = pack_bf16x2(p0, p1);
-              rs += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
-              pk[c] = w;
+              const float ks = lds_f32(sbase + C::kOffKScale + ((n & 3) * kPage + c0 + c) * 4);
+              y[c] = __float_as_uint(__uint_as_float(y[c]) * ks);
+              if (!((sees >> (c0 + c)) & 1)) y[c] = 0xff800000u;
             }
+          };
+          float mt = neg_inf();
+#pragma unroll 1
+          for (int c0 = 0; c0 < kPage; c0 += 16) {
+            uint32_t y[16];
+            scaled16(c0, y);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) mt = fmaxf(mt, __uint_as_float(y[c]));
           }
-          if (bad) {  // a value that is not finite was taken out of V: NaN for whoever sees it
+          if (!(ok = refer(mt))) break;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kPage; c0 += 16) {
+            uint32_t y[16], pk[8];
+            scaled16(c0, y);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              pk[c] = pack_bf16x2(ex2(fmaf(__uint_as_float(y[2 * c]), mul, -base)),
+                                  ex2(fmaf(__uint_as_float(y[2 * c + 1]), mul, -base)));
+              rs += __uint_as_float(pk[c] << 16) + __uint_as_float(pk[c] & 0xffff0000u);
+            }
+            tmem_st8(tS(sb) + lane_off + c0 / 2, pk);
+          }
+        }
+        if (__any_sync(kFull, bad != 0)) {  // a value was taken out of V: NaN for whoever sees it
+          tmem_wait_st();
+#pragma unroll 1
+          for (int c0 = 0; c0 < kPage / 2; c0 += 16) {
+            uint32_t y[16];
+            tmem_ld16(tS(sb) + lane_off + c0, y);
+            tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              if ((bad >> (c0 + 2 * c)) & 1) pk[c] = (pk[c] & 0xffff0000u) | 0x7fc0u;
-              if ((bad >> (c0 + 2 * c + 1)) & 1) pk[c] = (pk[c] & 0xffffu) | 0x7fc00000u;
+              if ((bad >> (2 * (c0 + c))) & 1) y[c] = (y[c] & 0xffff0000u) | 0x7fc0u;
+              if ((bad >> (2 * (c0 + c) + 1)) & 1) y[c] = (y[c] & 0xffffu) | 0x7fc00000u;
             }
+            tmem_st16(tS(sb) + lane_off + c0, y);
           }
-          tmem_st16(tS(sb) + lane_off + c0 / 2, pk);
         }
         l_sum = l_sum * alpha + rs;
         tmem_wait_st();
@@ -460,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
       }
       // ---- O / l.  Every warp waits here: Q is free for the next segment then.
       if (!ok) break;
-      ok = __all_sync(kFull, mbar_wait(b_o_final, seg & 1, abort_flag, a.wait_limit_ns) && !*abort_flag);
+      ok = __all_sync(kFull, mbar_poll(b_o_final, seg & 1, abort_flag, a.wait_limit_ns) && !*abort_flag);
       if (!ok) break;
       if (active) {
         tc_fence_after();
@@ -513,20 +570,25 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           // The operand is free first: then the MMAs of the tiles before are
           // issued, so the slot's last item (of the other warps, perhaps) is
           // used up and b_full cannot be a phase behind.
-          bool got = n == 0 || mbar_wait(b_free(is_v), (n - 1) & 1, abort_flag, a.wait_limit_ns);
-          if (got) got = mbar_wait(b_full(s), (i / C::kRing) & 1, abort_flag, a.wait_limit_ns);
+          bool got = n == 0 || mbar_poll(b_free(is_v), (n - 1) & 1, abort_flag, a.wait_limit_ns);
+          if (got) got = mbar_poll(b_full(s), (i / C::kRing) & 1, abort_flag, a.wait_limit_ns);
           if (!__all_sync(kFull, got)) {
             ok = false;
             break;
           }
           const uint32_t src = sbase + C::kOffRing + s * C::kSlot;
-          const uint32_t scales = sbase + C::kOffScale + s * C::kScaleBytes, v_scales = scales + kPage * 4;
+          const uint32_t scales = sbase + C::kOffScale + s * C::kScaleBytes;  // K, V
           const uint32_t dst = sbase + C::kOffConv + is_v * C::kTile;
           const bool zero = misc->bad_page[s] != 0;
+          bool fits = true;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) fits = fits && fits_f16(lds_f32(scales + (32 * x + lane) * 4));
+          const bool plain = __all_sync(kFull, fits || zero);
           // A thread takes 16-code chunks, eight neighbours the same chunk of
           // eight keys: with both tiles swizzled no read or write meets a bank twice.
-          constexpr int kChunks = D / 16;
+          constexpr int kChunks = D / 16, kM = kPage * kChunks / kN;
           const bool check = is_v && j >= first_tail;
+          const int key0 = (sg.t0 + j) * kPage;
           uint32_t bad0 = 0, bad1 = 0;  // keys 0-31 and 32-63
           auto place = [&](int m, int& key, int& c) {
             const int x = m * kN + t;
@@ -542,79 +604,60 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
             sts128(row + ((c2 ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
             sts128(row + (((c2 + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
           };
-          if (!is_v) {
-            if (t < kPage) {  // for softmax, which meets the scores after the tile's slot is free again
-              const float ks = zero ? 0.f : lds_f32(scales + t * 4);
-              reinterpret_cast<float*>(smem + C::kOffKScale)[(n & 3) * kPage + t] = ks;
-              const bool fits = __all_sync(kFull, zero || fits_f16(lds_f32(v_scales + t * 4)));
-              if (lane == 0) misc->f16[n & 3][w] = fits ? 1 : 0;
-            }
+          if (!is_v && t < kPage) {
+            if (!plain)  // for softmax
+              reinterpret_cast<float*>(smem + C::kOffKScale)[(n & 3) * kPage + t] = zero ? 0.f : lds_f32(scales + t * 4);
+            if (lane == 0) misc->plain[n & 3][w] = plain ? 1 : 0;
+          }
+          if (plain || !is_v) {
 #pragma unroll
-            for (int m = 0; m < kPage * kChunks / kN; ++m) {
+            for (int m = 0; m < kM; ++m) {
               int key, c;
               place(m, key, c);
-              const uint4 u = load(key, c);
-              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+              uint4 u = load(key, c);
+              float sc = plain ? lds_f32(scales + (is_v * kPage + key) * 4) : 1.f;
+              if (zero) sc = 0.f;
+              if (check && key0 + key >= sg.s.len) u = make_uint4(0, 0, 0, 0);
+              const uint32_t s2 = pack_f16x2(sc, sc), x[4] = {u.x, u.y, u.z, u.w};
               uint32_t o[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(x[e], o[2 * e], o[2 * e + 1]);
+              for (int e = 0; e < 4; ++e) {
+                e4m3x4_to_f16(x[e], o[2 * e], o[2 * e + 1]);
+                o[2 * e] = mul_f16x2(o[2 * e], s2);
+                o[2 * e + 1] = mul_f16x2(o[2 * e + 1], s2);
+              }
               store(key, c, o);
             }
           } else {
-            const int key0 = (sg.t0 + j) * kPage;
-            const bool f16 = __all_sync(kFull, zero || (fits_f16(lds_f32(v_scales + lane * 4)) &&
-                                                        fits_f16(lds_f32(v_scales + (lane + 32) * 4))));
-            if (f16) {
-#pragma unroll
-              for (int m = 0; m < kPage * kChunks / kN; ++m) {
-                int key, c;
-                place(m, key, c);
-                uint4 u = load(key, c);
-                const float sc = zero ? 0.f : lds_f32(v_scales + key * 4);
-                if (check && key0 + key >= sg.s.len) u = make_uint4(0, 0, 0, 0);
-                const uint32_t s2 = pack_f16x2(sc, sc), x[4] = {u.x, u.y, u.z, u.w};
-                uint32_t o[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  e4m3x4_to_f16(x[e], o[2 * e], o[2 * e + 1]);
-                  o[2 * e] = mul_f16x2(o[2 * e], s2);
-                  o[2 * e + 1] = mul_f16x2(o[2 * e + 1], s2);
-                }
-                store(key, c, o);
-              }
-            } else {
 #pragma unroll 1
-              for (int m = 0; m < kPage * kChunks / kN; ++m) {
-                int key, c;
-                place(m, key, c);
-                const uint4 u = load(key, c);
-                const float sc = lds_f32(v_scales + key * 4);
-                const uint32_t s2 = pack_bf16x2(sc, sc), x[4] = {u.x, u.y, u.z, u.w};
-                uint32_t o[8];
+            for (int m = 0; m < kM; ++m) {
+              int key, c;
+              place(m, key, c);
+              const uint4 u = load(key, c);
+              const float sc = lds_f32(scales + (kPage + key) * 4);
+              const uint32_t s2 = pack_bf16x2(sc, sc), x[4] = {u.x, u.y, u.z, u.w};
+              uint32_t o[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  o[2 * e] = mul_bf16x2(e4m3_hi_to_bf16x2(__byte_perm(x[e], 0, 0x1000)), s2);
-                  o[2 * e + 1] = mul_bf16x2(e4m3_hi_to_bf16x2(__byte_perm(x[e], 0, 0x3020)), s2);
-                }
-                if (check) {
-                  bool clear = key0 + key >= sg.s.len;
-                  bool nf = false;
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) nf |= has_nonfinite(o[e]);
-                  if (nf && !clear && key0 + key >= sg.s.prefix) {
-                    (key < 32 ? bad0 : bad1) |= 1u << (key & 31);
-                    clear = true;
-                  }
-                  if (clear) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = 0;
-                  }
-                }
-                store(key, c, o);
+              for (int e = 0; e < 4; ++e) {
+                o[2 * e] = mul_bf16x2(e4m3_hi_to_bf16x2(__byte_perm(x[e], 0, 0x1000)), s2);
+                o[2 * e + 1] = mul_bf16x2(e4m3_hi_to_bf16x2(__byte_perm(x[e], 0, 0x3020)), s2);
               }
+              if (check) {
+                bool clear = key0 + key >= sg.s.len;
+                bool nf = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) nf |= has_nonfinite(o[e]);
+                if (nf && !clear && key0 + key >= sg.s.prefix) {
+                  (key < 32 ? bad0 : bad1) |= 1u << (key & 31);
+                  clear = true;
+                }
+                if (clear) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) o[e] = 0;
+                }
+              }
+              store(key, c, o);
             }
-          }
-          if (check) {
             bad0 = __reduce_or_sync(kFull, bad0);
             bad1 = __reduce_or_sync(kFull, bad1);
           }
@@ -633,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
         // values that are not finite taken out (softmax makes up for them)
         for (int j = first_tail; j < sg.nt; ++j) {
           const int c = checks + j - first_tail;
-          if (!__all_sync(kFull, mbar_wait(b_drafted(c), (c / kChecks) & 1, abort_flag, a.wait_limit_ns))) {
+          if (!__all_sync(kFull, mbar_poll(b_drafted(c), (c / kChecks) & 1, abort_flag, a.wait_limit_ns))) {
             ok = false;
             break;
           }

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cstdlib>
 #include <cmath>
 #include <cstdint>
 
@@ -142,7 +143,8 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d) {
   const long long rows = static_cast<long long>(max_q) * (Hq / Hkv);
   // The least number of rows a CTA that holds all rows of a KV head, up to 32:
   // the warp-level MMAs' time grows with the rows.  Beyond, 128 on tcgen05.
-  p.per = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kManyRows;
+  p.per = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 32 : kManyRows;
+  if (getenv("TREE_PER")) p.per = atoi(getenv("TREE_PER"));
   p.planes = static_cast<int>((rows + p.per - 1) / p.per);
   const long long tiles = (L + kPage - 1) / kPage;
   p.min_tiles = 4;
