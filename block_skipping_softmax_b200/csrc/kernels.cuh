@@ -98,7 +98,7 @@ struct TreeLaunch {
   float scale_log2;
   int planes;     // row blocks of the longest draft: grid.y
   int ctas;       // CTAs of a plane: grid.x
-  int min_tiles;  // least work of a CTA
+  int min_tiles;  // least work of a CTA; 0: no KV head's tiles are divided
   float* part;    // [planes, ctas, 2, rows of a CTA, d] fp32: shares of a KV head's keys
   float* lse;     // [planes, ctas, 2, rows of a CTA]
   int* status;
@@ -106,9 +106,9 @@ struct TreeLaunch {
   cudaStream_t stream;
 };
 
-// rows of a CTA: 8, 16 or 32 (tree_few_sm100.cu), with so many CTAs an SM
+// rows of a CTA: 8, or 16 over e4m3 (tree_few_sm100.cu), with so many CTAs an SM
 int launch_tree_few(const TreeLaunch& a, int rows);
-int tree_few_ctas(int rows);
+int tree_few_ctas();
 int launch_tree_many(const TreeLaunch& a);  // 128 rows, 2 CTAs an SM (tree_many_sm100.cu)
 
 // Current device (sm_100 checked) and its device status word (api.cu).

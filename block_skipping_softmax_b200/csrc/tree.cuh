@@ -135,50 +135,96 @@ __device__ __forceinline__ Seq seq_of(const TreeLaunch& a, int b) {
 }
 
 // The work of one plane (row block `plane` of every sequence that has one) is
-// the line of all its tiles: sequences, KV heads and tiles, in this order.  Its
-// CTAs take equal pieces of that line, whatever the sequences' lengths, so a
-// ragged batch keeps every SM busy to the end.  A piece consists of segments,
-// runs of tiles of one KV head; a segment that is not all of its KV head's
-// tiles leaves a share of the result in one of the CTA's two places (only its
-// first and its last segment can be one), which tree_merge_kernel adds up.  A
-// sequence without keys counts as one tile, so that its zeros get written.
+// the line of all its tiles: sequences, KV heads and tiles, in this order.  It
+// is divided among the plane's CTAs in one of two ways.
+//   By heads: every KV head's tiles go to `shares` CTAs of their own.
+//   Equal pieces: the line is cut into pieces that differ by one tile at most,
+//   whatever the sequences' lengths, so a ragged batch keeps every SM busy to
+//   the end.  A piece consists of segments, runs of tiles of one KV head.
+// A segment has its own start and end (queries, first copies, adding up the
+// warps' sums), worth about kSegment tiles, and a piece has two of them mostly.  So
+// heads are kept whole unless their longest share is longer than an equal piece
+// by more than that.
+//
+// A segment that is not all of its KV head's tiles leaves a share of the result
+// in one of the CTA's two places (only its first and its last segment can be
+// one), which tree_merge_kernel adds up.  A sequence without keys counts as one
+// tile, so that its zeros get written.
 //
 // Planes run side by side over the same line, so that row blocks that read the
 // same pages do so at about the same time, from L2.
-// A plane has fewer than 2^31 tiles (the host checks B * max_seq_len * Hkv).
+constexpr int kSegment = 6;
+
+// 32 sequences of the line; a plane has fewer than 2^31 tiles (the host checks
+// B * max_seq_len * Hkv).
 struct Line {
-  int w, incl, before;  // this lane's sequence of the chunk, sum up to it, sum before the chunk
+  int tiles;             // of this lane's sequence, at least 1; 0: it has no rows on the plane
+  int incl, before;      // tiles of all heads up to it, and before the chunk
+  unsigned active;       // lanes with rows
+  int heads;             // KV heads before the chunk
   int chunk;
 
-  __device__ __forceinline__ static int work_of(const TreeLaunch& a, const Seq& s, int first_row) {
-    if (s.T * (a.Hq / a.Hkv) <= first_row) return 0;
-    return max(1, (s.len + kPage - 1) / kPage) * a.Hkv;
-  }
-  // Warp-collective: 32 sequences from `at` on.
-  __device__ __forceinline__ void load(const TreeLaunch& a, int first_row, int at, int sum) {
+  // Warp-collective: the sequences from `at` on.
+  __device__ __forceinline__ void load(const TreeLaunch& a, int first_row, int at, int tiles_before, int heads_before) {
     const int lane = threadIdx.x & 31;
     chunk = at;
-    before = sum;
-    w = 0;
-    if (at + lane < a.B) w = work_of(a, seq_of(a, at + lane), first_row);
-    incl = w;
+    before = tiles_before;
+    heads = heads_before;
+    tiles = 0;
+    if (at + lane < a.B) {
+      const Seq s = seq_of(a, at + lane);
+      if (s.T * (a.Hq / a.Hkv) > first_row) tiles = max(1, (s.len + kPage - 1) / kPage);
+    }
+    active = __ballot_sync(kFull, tiles > 0);
+    incl = tiles * a.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += x;
     }
   }
+  __device__ __forceinline__ void next(const TreeLaunch& a, int first_row) {
+    load(a, first_row, chunk + 32, before + total(), heads + __popc(active) * a.Hkv);
+  }
   __device__ __forceinline__ int total() const { return __shfl_sync(kFull, incl, 31); }
+  // KV heads before lane l's sequence
+  __device__ __forceinline__ int heads_at(const TreeLaunch& a, int l) const {
+    return heads + __popc(active & ((1u << l) - 1)) * a.Hkv;
+  }
 };
 
-// How W tiles are divided among CTAs: `used` of them, the first `more` with one
-// tile more than the others' `each`.
-struct Pieces {
-  int used, each, more;
-  __device__ __forceinline__ Pieces(const TreeLaunch& a, int W) {
+struct Division {
+  int shares;            // by heads: CTAs of a head; 0: equal pieces
+  int used, each, more;  // equal pieces: CTAs, the first `more` with one tile more than `each`
+
+  // Warp-collective; leaves the line at its first chunk.
+  __device__ __forceinline__ Division(const TreeLaunch& a, int first_row, Line& line) {
+    line.load(a, first_row, 0, 0, 0);
+    int most = line.tiles;
+    while (line.chunk + 32 < a.B) {
+      line.next(a, first_row);
+      most = max(most, line.tiles);
+    }
+    most = __reduce_max_sync(kFull, most);
+    const int W = line.before + line.total(), heads = line.heads + __popc(line.active) * a.Hkv;
+    if (a.B > 32) line.load(a, first_row, 0, 0, 0);
+    shares = used = each = more = 0;
+    if (W == 0) return;
+    if (a.min_tiles == 0) {
+      shares = 1;
+      used = heads;
+      return;
+    }
     used = max(1, min(a.ctas, (W - 1) / a.min_tiles + 1));
     each = W / used;
     more = W - each * used;
+    if (heads <= a.ctas) {
+      const int n = min(a.ctas / heads, (most - 1) / a.min_tiles + 1);
+      if ((most - 1) / n + 1 <= each + kSegment) {
+        shares = n;
+        used = heads * n;
+      }
+    }
   }
   __device__ __forceinline__ int first(int cta) const { return each * cta + min(cta, more); }
   __device__ __forceinline__ int cta_of(int tile) const {
@@ -199,44 +245,61 @@ struct Segment {
 // The segments of this CTA, for every warp by itself (all calls warp-collective).
 struct Segments {
   Line line;
-  int begin, pos, end;
+  int shares, begin, pos, end;  // by heads: begin is the share, pos the KV head, end one further
 
   __device__ __forceinline__ void start(const TreeLaunch& a, int per) {
-    const int row0 = blockIdx.y * per;
-    line.load(a, row0, 0, 0);
-    int W = line.total();
-    if (a.B > 32) {
-      for (int at = 32; at < a.B; at += 32) {
-        line.load(a, row0, at, W);
-        W += line.total();
-      }
-      line.load(a, row0, 0, 0);
-    }
+    const Division d(a, blockIdx.y * per, line);
+    const int i = blockIdx.x;
+    shares = d.shares;
     begin = pos = end = 0;
-    if (W == 0) return;
-    const Pieces p(a, W);
-    if (static_cast<int>(blockIdx.x) < p.used) {
-      begin = pos = p.first(blockIdx.x);
-      end = p.first(blockIdx.x + 1);
+    if (i >= d.used) return;
+    if (shares) {
+      pos = i / shares;
+      begin = i - pos * shares;
+      end = pos + 1;
+    } else {
+      begin = pos = d.first(i);
+      end = d.first(i + 1);
     }
   }
   __device__ __forceinline__ bool next(const TreeLaunch& a, int per, Segment& g) {
     if (pos >= end) return false;
     const int row0 = blockIdx.y * per;
-    while (pos >= line.before + line.total()) line.load(a, row0, line.chunk + 32, line.before + line.total());
-    const int l = __ffs(__ballot_sync(kFull, pos < line.before + line.incl)) - 1;
-    const int first = line.before + __shfl_sync(kFull, line.incl - line.w, l);
+    int l, first;  // the lane of the sequence; its first KV head, or tile of the line
+    if (shares) {
+      while (pos >= line.heads + __popc(line.active) * a.Hkv) line.next(a, row0);
+      const int lane = threadIdx.x & 31, mine = line.heads_at(a, lane);
+      l = __ffs(__ballot_sync(kFull, ((line.active >> lane) & 1) && pos >= mine && pos < mine + a.Hkv)) - 1;
+      first = line.heads_at(a, l);
+    } else {
+      while (pos >= line.before + line.total()) line.next(a, row0);
+      l = __ffs(__ballot_sync(kFull, pos < line.before + line.incl)) - 1;
+      first = line.before + __shfl_sync(kFull, line.incl - line.tiles * a.Hkv, l);
+    }
     g.b = line.chunk + l;
     g.s = seq_of(a, g.b);
     const int tiles = (g.s.len + kPage - 1) / kPage, span = max(1, tiles);
+    g.row0 = row0;
+    g.rows = min(per, g.s.T * (a.Hq / a.Hkv) - row0);
+    if (shares) {
+      const int share = begin;
+      g.kv = pos - first;
+      ++pos;
+      const int from = static_cast<int>(static_cast<long long>(span) * share / shares);
+      const int to = static_cast<int>(static_cast<long long>(span) * (share + 1) / shares);
+      if (from == to) return false;  // fewer tiles than shares
+      g.t0 = from;
+      g.nt = min(to, tiles) - from;
+      g.whole = to - from == span;
+      g.place = 0;
+      return true;
+    }
     g.kv = (pos - first) / span;
     g.t0 = pos - first - g.kv * span;
     const int n = min(span - g.t0, end - pos);
     g.nt = min(n, tiles - g.t0);
     g.whole = n == span;
     g.place = pos == begin ? 0 : 1;
-    g.row0 = row0;
-    g.rows = min(per, g.s.T * (a.Hq / a.Hkv) - row0);
     pos += n;
     return true;
   }

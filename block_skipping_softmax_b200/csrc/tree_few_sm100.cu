@@ -33,20 +33,20 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kCtas = 3;  // of an SM
 
 template <int D, bool E4M3, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtas = NT == 4 ? 2 : 3;                // of an SM
   static constexpr int kRowBytes = E4M3 ? D : 2 * D;
-  static constexpr int kKB = kRowBytes == 256 || (kRowBytes == 128 && E4M3 && NT == 4) ? 1 : 2;         // blocks of 16 keys that a warp takes of a page
+  static constexpr int kKB = kRowBytes == 256 ? 1 : 2;         // blocks of 16 keys that a warp takes of a page
   static constexpr int kKeys = 16 * kKB;
   static constexpr int kShare = kPage / kKeys;                 // warps that share a page
   static constexpr int kEvery = kWarps / kShare;               // a warp takes every kEvery-th page
   static constexpr int kTile = kKeys * kRowBytes;              // a warp's keys (or values) of a page
   static constexpr int kPanels = E4M3 ? 1 : D / 64;            // swizzled panels of it
   static constexpr int kScaleBytes = E4M3 ? kKeys * 4 : 0;
-  static constexpr int kStages = (kRowBytes == 64 ? 4 : 2) * (kKB == 1 && kRowBytes != 256 ? 2 : 1);
+  static constexpr int kStages = kRowBytes == 64 ? 4 : 2;
   static constexpr int kStageBytes = 2 * kTile;
   static constexpr int kOffScale = kWarps * kStages * kStageBytes;  // [warp][stage][K, V][keys] floats
   static constexpr int kOffRed = kOffScale + kWarps * kStages * 2 * kScaleBytes;  // rows x D floats
@@ -94,7 +94,7 @@ struct Lanes {
 };
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, E4M3, NT>::kCtas)
+__global__ void __launch_bounds__(kThreads, kCtas)
     tree_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ TreeLaunch a) {
   using C = Cfg<D, E4M3, NT>;
@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, E4M3, NT>::kCtas)
   const uint32_t ring_scale = sbase + C::kOffScale + warp * C::kStages * 2 * C::kScaleBytes;
   const int part = warp % C::kShare, first_page = warp / C::kShare;  // this warp's keys of a page, its pages
 
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may look for its shares
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8 * s, 1);
@@ -676,14 +677,15 @@ template <int D, bool E4M3>
 int launch_n(const TreeLaunch& a, int rows) {
   switch (rows) {
     case 8: return launch_t<D, E4M3, 1>(a);
-    case 16: return launch_t<D, E4M3, 2>(a);
-    default: return launch_t<D, E4M3, 4>(a);
+    case 16:
+      if constexpr (E4M3) return launch_t<D, E4M3, 2>(a);
   }
+  return ATTN_ERR_INVALID_ARG;
 }
 
 }  // namespace
 
-int tree_few_ctas(int rows) { return rows == 32 ? Cfg<128, true, 4>::kCtas : Cfg<128, true, 1>::kCtas; }
+int tree_few_ctas() { return kCtas; }
 
 int launch_tree_few(const TreeLaunch& a, int rows) {
   if (a.d == 64) return a.k_scales ? launch_n<64, true>(a, rows) : launch_n<64, false>(a, rows);

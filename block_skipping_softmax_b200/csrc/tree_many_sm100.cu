@@ -1,13 +1,17 @@
 // Tree attention for many rows a KV head: 128 rows a CTA on tcgen05.
 //
-//   warp 0       copies: K and V pages, a ring in shared memory
-//   warp 1       TMEM, and the one thread that issues the MMAs:
+//   warp 0       finds the CTA's segments and passes them on to the others
+//   warp 1       bf16 pool: checks the V tiles that hold drafted keys
+//   warp 2       copies: K and V pages, a ring in shared memory
+//   warp 3       TMEM, and the one thread that issues the MMAs:
 //                  S_j = Q K_j^T (two buffers), O += P_j V_j (P read from TMEM)
 //   warps 4-7    softmax: a thread owns the row of TMEM lane 32 (warp % 4) + lane
-//   tile warps   bf16 pool: warps 2 and 3 check the V tiles that hold drafted
-//                keys.  e4m3: warps 8-11 turn codes of K into an fp16 operand and
-//                warps 12-15 codes of V into an fp16 (rarely bf16) one; the
-//                registers are divided anew between the roles
+//   warps 8-15   e4m3: 8-11 turn codes of K into an fp16 operand, 12-15 codes of
+//                V into an fp16 (rarely bf16) one; the registers are divided
+//                anew between the roles
+//
+// (The issuer and the copies are not on the schedulers of softmax warps 4 and 5,
+// which are the busy ones with up to 64 rows.)
 //
 // A tile is one page of 64 keys, so that TMEM holds O and two S in 256 columns
 // and two CTAs share an SM: one's softmax runs beside the other's MMAs.  Every
@@ -29,12 +33,14 @@ namespace bss {
 namespace {
 
 constexpr int kRows = kManyRows;
+constexpr int kSegs = 4;    // segments on their way from warp 0 to the others
 constexpr int kChecks = 4;  // tiles with drafted keys on their way: see Tails
 
 template <int D, bool E4M3>
 struct Cfg {
-  static constexpr int kPrep = E4M3 ? 4 : 2;  // warps that convert K, convert V or check V tiles
-  static constexpr int kPrepWarp = E4M3 ? 8 : 2;
+  static constexpr int kPrep = E4M3 ? 4 : 1;  // warps that convert K, convert V or check V tiles
+  static constexpr int kPrepWarp = E4M3 ? 8 : 1;
+  static constexpr int kReaders = E4M3 ? 14 : 7;  // warps that follow the segments
   static constexpr int kThreads = E4M3 ? 512 : 256;
   // Registers a thread, e4m3: 64 at launch, then by warpgroup (copies and MMAs,
   // softmax, tiles, tiles), 256 in all.
@@ -46,17 +52,19 @@ struct Cfg {
   static constexpr int kRing = E4M3 ? (D == 128 ? 5 : 8) : (D == 128 ? 4 : 6);  // tiles in flight
   static constexpr int kSlot = E4M3 ? kRaw : kTile;
   static constexpr int kOffQ = 0;
+  static constexpr int kOperands = D == 64 ? 2 : 1;                // e4m3: buffers of each operand
   static constexpr int kOffConv = kOffQ + kRows * D * 2;           // e4m3: K and V operands
-  static constexpr int kOffRing = kOffConv + (E4M3 ? 2 * kTile : 0);
+  static constexpr int kOffRing = kOffConv + (E4M3 ? 2 * kOperands * kTile : 0);
   static constexpr int kScaleBytes = E4M3 ? 2 * kPage * 4 : 0;    // K, V
   static constexpr int kOffScale = kOffRing + kRing * kSlot;       // e4m3: [slot][K, V][64] floats
   static constexpr int kOffKScale = kOffScale + kRing * kScaleBytes;  // e4m3: [4][64], for softmax
   static constexpr int kOffBar = kOffKScale + (E4M3 ? 4 * kPage * 4 : 0);
   // full[ring], empty[ring], q_full, s_full[2], p_full[2], pv_done, o_final,
-  // checked[4]; bf16: drafted[4]; e4m3: ready[K, V], free[K, V]
-  static constexpr int kBars = 2 * kRing + 7 + 2 * kChecks;
+  // checked[4]; bf16: drafted[4]; e4m3: ready[K, V][buffers], free[K, V][buffers];
+  // segment full[4], segment empty[4]
+  static constexpr int kBars = 2 * kRing + 7 + 3 * kChecks + 2 * kSegs;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
-  static constexpr int kMiscBytes = 224;
+  static constexpr int kMiscBytes = 432;
   static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;
   static constexpr int kTmemCols = 256;
   static_assert(D + 2 * kPage <= kTmemCols, "O and two S");
@@ -67,6 +75,7 @@ struct Misc {
   uint32_t tmem_base;
   int abort;
   int bad_page[8];  // e4m3: the slot's page id was out of range
+  int segs[kSegs][12];
   int plain[4][2];  // e4m3, by tile: whether the scales of keys 0-31, 32-63 fit fp16 operands
 };
 
@@ -113,9 +122,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
   // V tile number c with drafted keys (over the CTA's segments) is checked; bf16: has landed
   auto b_checked = [&](int c) { return bar1 + 8u * (7 + c % kChecks); };
   auto b_drafted = [&](int c) { return bar1 + 8u * (7 + kChecks + c % kChecks); };
-  // e4m3: K (0) or V (1) is converted, its MMAs are done
-  auto b_ready = [&](int v) { return bar1 + 8u * (7 + kChecks + v); };
-  auto b_free = [&](int v) { return bar1 + 8u * (9 + kChecks + v); };
+  // e4m3: K (0) or V (1) of tile n is converted, its MMAs are done
+  auto b_ready = [&](int v, int n) { return bar1 + 8u * (7 + kChecks + 2 * v + n % C::kOperands); };
+  auto b_free = [&](int v, int n) { return bar1 + 8u * (11 + kChecks + 2 * v + n % C::kOperands); };
+
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may look for its shares
+  auto b_seg_full = [&](int i) { return bar1 + 8u * (7 + 3 * kChecks + i % kSegs); };
+  auto b_seg_empty = [&](int i) { return bar1 + 8u * (7 + 3 * kChecks + kSegs + i % kSegs); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -128,13 +141,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
       mbar_init(b_s_full(i), 1);
       mbar_init(b_p_full(i), 4);
       if constexpr (E4M3) {
-        mbar_init(b_ready(i), C::kPrep);
-        mbar_init(b_free(i), 1);
+        for (int n = 0; n < C::kOperands; ++n) {
+          mbar_init(b_ready(i, n), C::kPrep);
+          mbar_init(b_free(i, n), 1);
+        }
       }
     }
     for (int i = 0; i < kChecks; ++i) {
       mbar_init(b_checked(i), C::kPrep);
       if constexpr (!E4M3) mbar_init(b_drafted(i), 1);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(b_seg_full(i), 1);
+      mbar_init(b_seg_empty(i), C::kReaders);
     }
     mbar_init(b_pv_done, 1);
     mbar_init(b_o_final, 1);
@@ -142,12 +161,12 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
+  if (warp == 3) {
     tmem_alloc(smem_u32(&misc->tmem_base), C::kTmemCols);
     tmem_relinquish();
   }
   Segments list;
-  list.start(a, kRows);
+  if (warp == 0) list.start(a, kRows);
   Segment sg{};
   tc_fence_before();
   __syncthreads();
@@ -170,11 +189,59 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
   auto tail0 = [&] { return max(sg.s.prefix / kPage - sg.t0, 0); };
   auto tails = [&] { return max(sg.nt - tail0(), 0); };
 
+  // ------------------------------------------------ segments
+  auto segments = [&] {
+    bool more = true;
+    for (int i = 0; more; ++i) {
+      more = list.next(a, kRows, sg);
+      if (i >= kSegs && !__all_sync(kFull, mbar_poll(b_seg_empty(i), (i / kSegs - 1) & 1, abort_flag,
+                                                     a.wait_limit_ns))) {
+        if (lane == 0) give_up(50);
+        break;
+      }
+      if (lane == 0) {
+        volatile int* p = misc->segs[i % kSegs];
+        p[0] = more ? sg.nt : -1;
+        p[1] = sg.b;
+        p[2] = sg.kv;
+        p[3] = sg.t0;
+        p[4] = sg.rows;
+        p[5] = sg.whole ? 1 : 0;
+        p[6] = sg.place;
+        p[7] = sg.s.tok0;
+        p[8] = sg.s.len;
+        p[9] = sg.s.prefix;
+        mbar_arrive(b_seg_full(i));
+      }
+    }
+  };
+  auto next_segment = [&](int i) {
+    if (!__all_sync(kFull, mbar_poll(b_seg_full(i), (i / kSegs) & 1, abort_flag, a.wait_limit_ns))) {
+      if (lane == 0) give_up(51);
+      return false;
+    }
+    const volatile int* p = misc->segs[i % kSegs];
+    sg.nt = p[0];
+    sg.b = p[1];
+    sg.kv = p[2];
+    sg.t0 = p[3];
+    sg.rows = p[4];
+    sg.whole = p[5] != 0;
+    sg.place = p[6];
+    sg.s.tok0 = p[7];
+    sg.s.len = p[8];
+    sg.s.prefix = p[9];
+    sg.row0 = blockIdx.y * kRows;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_seg_empty(i));
+    return sg.nt >= 0;
+  };
+
   // ------------------------------------------------ copies
   auto copies = [&] {
     int issued = 0, checks = 0, landed = 0;  // items, drafted tiles, drafted tiles issued
     bool ok = true;
-    while (ok && list.next(a, kRows, sg)) {
+    for (int seg = 0; ok && next_segment(seg); ++seg) {
       const int* table = a.block_table + static_cast<size_t>(sg.b) * a.max_pages + sg.t0;
       int pages_k = 0, pages_v = 0;  // lane i: the page of tile i + 32 n, for the K and the V stream
       const int first_tail = tail0();
@@ -245,23 +312,24 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
       give_up(site);
       return false;
     };
+    int slot = 0, phase = 0;  // bf16: the ring's items are used in its order
     // descriptors: the high words are constants, an MMA adds offsets to the low ones
     constexpr uint32_t hi = sw128_desc_hi(1024);
     const uint32_t dQ = sw128_desc_lo(sbase + C::kOffQ, 16);
     const uint32_t dK = sw128_desc_lo(sbase + (E4M3 ? C::kOffConv : C::kOffRing), 16);
-    const uint32_t dV = sw128_desc_lo(sbase + (E4M3 ? C::kOffConv + C::kTile : C::kOffRing), C::kTilePanel);
+    const uint32_t dV = sw128_desc_lo(sbase + (E4M3 ? C::kOffConv + C::kOperands * C::kTile : C::kOffRing), C::kTilePanel);
+    auto buffer = [&](int n) { return (E4M3 ? n % C::kOperands : slot) * ((E4M3 ? C::kTile : C::kSlot) >> 4); };
     bool ok = true;
     int seg = 0, n0 = 0, checks = 0;  // segments, tiles and drafted tiles before this one
-    int slot = 0, phase = 0;          // bf16: the ring's items are used in its order
-    while (ok && list.next(a, kRows, sg)) {
+    while (ok && next_segment(seg)) {
       if (lane == 0) {
         const int nt = sg.nt, first_tail = tail0();
         ok = wait(b_q_full, seg & 1, 41);
         for (int j = 0; ok && nt > 0 && j <= nt; ++j) {
           if (j < nt) {
             const int n = n0 + j;
-            const uint32_t at = E4M3 ? dK : dK + slot * (C::kSlot >> 4);
-            if (!(ok = E4M3 ? wait(b_ready(0), n & 1, 42) : wait(b_full(slot), phase, 42))) break;
+            const uint32_t at = dK + buffer(n);
+            if (!(ok = E4M3 ? wait(b_ready(0, n), (n / C::kOperands) & 1, 42) : wait(b_full(slot), phase, 42))) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -270,13 +338,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
                      desc_join(at + (kk >> 2) * (C::kTilePanel >> 4) + (kk & 3) * kStep, hi), idS, kk > 0 ? 1u : 0u);
             }
             mma_commit(b_s_full(n & 1));
-            mma_commit(E4M3 ? b_free(0) : b_empty(slot));
+            mma_commit(E4M3 ? b_free(0, n) : b_empty(slot));
             if (++slot == C::kRing) slot = 0, phase ^= 1;
           }
           if (j >= 1) {
             const int t = j - 1, n = n0 + t;
-            const uint32_t at = E4M3 ? dV : dV + slot * (C::kSlot >> 4);
-            if (!(ok = E4M3 ? wait(b_ready(1), n & 1, 43) : wait(b_full(slot), phase, 43))) break;
+            const uint32_t at = dV + buffer(n);
+            if (!(ok = E4M3 ? wait(b_ready(1, n), (n / C::kOperands) & 1, 43) : wait(b_full(slot), phase, 43))) break;
             if (!E4M3 && t >= first_tail) {
               const int c = checks + t - first_tail;
               if (!(ok = wait(b_checked(c), (c / kChecks) & 1, 44))) break;
@@ -287,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
 #pragma unroll
             for (int kk = 0; kk < kPage / 16; ++kk)
               mma_ts(tO, tS(n & 1) + kk * 8, desc_join(at + kk * (16 * 128 >> 4), hi), id, (t > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(E4M3 ? b_free(1) : b_empty(slot));
+            mma_commit(E4M3 ? b_free(1, n) : b_empty(slot));
             mma_commit(b_pv_done);
             if (++slot == C::kRing) slot = 0, phase ^= 1;
           }
@@ -307,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     bool ok = true;
     int seg = 0, n0 = 0, checks = 0;
-    while (ok && list.next(a, kRows, sg)) {
+    while (ok && next_segment(seg)) {
       const bool valid = r < sg.rows;
       const bool active = (warp & 3) * 32 < sg.rows;  // some row of the warp
       int tok = 0;
@@ -561,7 +629,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
     const int t = (threadIdx.x - C::kPrepWarp * 32) % kN, w = (warp - C::kPrepWarp) % C::kPrep;
     bool ok = true;
     int n0 = 0, item0 = 0, checks = 0;
-    while (ok && list.next(a, kRows, sg)) {
+    for (int seg = 0; ok && next_segment(seg); ++seg) {
       const int first_tail = tail0();
       if constexpr (E4M3) {
         const int is_v = warp >= C::kPrepWarp + C::kPrep ? 1 : 0;
@@ -570,7 +638,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           // The operand is free first: then the MMAs of the tiles before are
           // issued, so the slot's last item (of the other warps, perhaps) is
           // used up and b_full cannot be a phase behind.
-          bool got = n == 0 || mbar_poll(b_free(is_v), (n - 1) & 1, abort_flag, a.wait_limit_ns);
+          bool got = n < C::kOperands ||
+                     mbar_poll(b_free(is_v, n), (n / C::kOperands - 1) & 1, abort_flag, a.wait_limit_ns);
           if (got) got = mbar_poll(b_full(s), (i / C::kRing) & 1, abort_flag, a.wait_limit_ns);
           if (!__all_sync(kFull, got)) {
             ok = false;
@@ -578,7 +647,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           }
           const uint32_t src = sbase + C::kOffRing + s * C::kSlot;
           const uint32_t scales = sbase + C::kOffScale + s * C::kScaleBytes;  // K, V
-          const uint32_t dst = sbase + C::kOffConv + is_v * C::kTile;
+          const uint32_t dst = sbase + C::kOffConv + (is_v * C::kOperands + n % C::kOperands) * C::kTile;
           const bool zero = misc->bad_page[s] != 0;
           bool fits = true;
 #pragma unroll
@@ -667,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(b_empty(s));
-            mbar_arrive(b_ready(is_v));
+            mbar_arrive(b_ready(is_v, n));
             if (check) mbar_arrive(b_checked(c));
           }
         }
@@ -712,8 +781,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
   if (warp < 4) {
     if constexpr (E4M3) reg_dec<C::kRegsIssue>();
     if (warp == 0)
+      segments();
+    else if (warp == 2)
       copies();
-    else if (warp == 1)
+    else if (warp == 3)
       issue();
     else if constexpr (!E4M3)
       tiles();
@@ -727,7 +798,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tO, C::kTmemCols);
   }

@@ -16,7 +16,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <cstdlib>
 #include <cmath>
 #include <cstdint>
 
@@ -43,26 +42,35 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   const int group = a.Hq / a.Hkv, head = r % a.Hq;
   const int kv = head / group, row = (r / a.Hq) * group + head % group;  // row of the KV head
   const int plane = row / per;
-  // this KV head's place on its plane's line
+  // this KV head's shares: CTAs c0 to c1, of which the first may be in the CTA's
+  // second place
   Line line;
-  int total = 0, first = 0;
-  for (int at = 0; at < a.B; at += 32) {
-    line.load(a, plane * per, at, total);
-    if (b >= at && b < at + 32) first = total + __shfl_sync(kFull, line.incl - line.w, b - at);
-    total += line.total();
-  }
-  if (r >= s.T * a.Hq) return;  // the same for all warps of a row
+  const Division div(a, plane * per, line);
+  while (b >= line.chunk + 32) line.next(a, plane * per);
   const int span = max(1, (s.len + kPage - 1) / kPage);
-  first += kv * span;
-  const Pieces p(a, total);
-  const int c0 = p.cta_of(first), c1 = p.cta_of(first + span - 1);
-  if (c0 == c1) return;
-  // only the first share can be a CTA's last segment, and not its first
-  const int place0 = p.first(c0) >= first ? 0 : 1;
+  const int head_at = line.heads_at(a, b - line.chunk) + kv;
+  const int first = line.before + __shfl_sync(kFull, line.incl - line.tiles * a.Hkv, b - line.chunk) + kv * span;
+  if (r >= s.T * a.Hq) return;  // the same for all warps of a row
+  int c0, c1, place0 = 0;
+  if (div.shares) {
+    c0 = head_at * div.shares;
+    c1 = c0 + div.shares - 1;
+  } else {
+    c0 = div.cta_of(first);
+    c1 = div.cta_of(first + span - 1);
+    place0 = div.first(c0) >= first ? 0 : 1;
+  }
+  if (c0 == c1 || (div.shares && span == 1)) return;
+  // with fewer tiles than shares, share i is empty unless it ends behind i's start
+  auto empty = [&](int c) {
+    const long long i = c - c0;
+    return div.shares > span && span * i / div.shares == span * (i + 1) / div.shares;
+  };
   auto share = [&](int c) { return share_at(a, per, plane, c, c == c0 ? place0 : 0, row - plane * per); };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float M = neg_inf();
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.lse[share(c)]);
+  for (int c = c0 + lane; c <= c1; c += 32)
+    if (!empty(c)) M = fmaxf(M, a.lse[share(c)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
   constexpr int kC = D / 32;
@@ -72,7 +80,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   for (int base = c0 + part; base <= c1; base += 32 * W) {
     // lane i: weight of share base + i W
     float w = 0.f;
-    if (base + lane * W <= c1) {
+    if (base + lane * W <= c1 && !empty(base + lane * W)) {
       const float l = a.lse[share(base + lane * W)];
       w = l == neg_inf() ? 0.f : l == M ? 1.f : ex2(l - M);  // 0: nothing seen there
     }
@@ -81,6 +89,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(kFull, w, i);
+      if (wi == 0.f) continue;  // an empty share, perhaps: its sums were not written
       const float* x = a.part + share(base + i * W) * D + lane * kC;
 #pragma unroll
       for (int e = 0; e < kC; e += 2) {
@@ -138,21 +147,29 @@ struct Plan {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d) {
+Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
   Plan p{};
   const long long rows = static_cast<long long>(max_q) * (Hq / Hkv);
-  // The least number of rows a CTA that holds all rows of a KV head, up to 32:
-  // the warp-level MMAs' time grows with the rows.  Beyond, 128 on tcgen05.
-  p.per = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 32 : kManyRows;
-  if (getenv("TREE_PER")) p.per = atoi(getenv("TREE_PER"));
+  p.per = rows <= 8 ? 8 : rows <= 16 && e4m3 ? 16 : kManyRows;
   p.planes = static_cast<int>((rows + p.per - 1) / p.per);
-  const long long tiles = (L + kPage - 1) / kPage;
-  p.min_tiles = 4;
-  const long long slots = 148 * (p.per < kManyRows ? tree_few_ctas(p.per) : 2);
-  const long long most = (tiles * B * Hkv + p.min_tiles - 1) / p.min_tiles;
+  const long long tiles = (L + kPage - 1) / kPage, heads = static_cast<long long>(B) * Hkv;
+  const long long slots = 148 * (p.per < kManyRows ? tree_few_ctas() : 2);
   const long long fit = p.planes < slots ? slots / p.planes : 1;
+  // A CTA for each KV head, and no merge, where its tiles are few, or where the
+  // heads are more than the CTAs that run at once and rounds of them cost less
+  // than equal pieces: in tiles, rounds * (tiles + kSegment) against the equal piece
+  // and its segments.
+  const long long rounds = (heads + fit - 1) / fit;
+  if (tiles <= 8 || (rounds > 1 && 2 * rounds * (tiles + kSegment) <
+                                       2 * (heads * tiles / fit) + (2 * heads / fit + 3) * kSegment)) {
+    p.min_tiles = 0;
+    p.ctas = static_cast<int>(heads);
+    return p;
+  }
+  p.min_tiles = 4;
+  const long long most = (tiles * heads + p.min_tiles - 1) / p.min_tiles;
   p.ctas = static_cast<int>(most < fit ? most : fit);
-  p.shares = tiles > 1 && p.ctas > 1;
+  p.shares = p.ctas > 1;
   if (p.shares) {
     const size_t n = static_cast<size_t>(p.planes) * p.ctas * 2 * p.per;
     p.part_bytes = align256(n * d * sizeof(float));
@@ -183,7 +200,7 @@ int run_tree(TreeLaunch& a, void* ws, size_t ws_bytes, void* stream) {
   // one group past the pool's end is addressed for a page id out of range
   if ((static_cast<long long>(a.num_pages) + 1) * a.Hkv > 0x7fffffffLL || a.max_pages > 0x7fffffff / kPage)
     return ATTN_ERR_UNSUPPORTED;
-  const Plan p = plan_of(a.B, a.max_q, a.Hq, a.Hkv, a.L, a.d);
+  const Plan p = plan_of(a.B, a.max_q, a.Hq, a.Hkv, a.L, a.d, a.k_scales != nullptr);
   if (p.shares) {
     if (!ws || !ptr_aligned(ws, 256) || ws_bytes < p.bytes) return ATTN_ERR_INVALID_ARG;
     a.part = static_cast<float*>(ws);
@@ -233,7 +250,10 @@ extern "C" {
 size_t attn_tree_workspace_bytes(int B, int max_q, int total_q, int Hq, int Hkv, int max_seq_len, int d) {
   using namespace bss;
   if (check_sizes(B, max_q, total_q, Hq, Hkv, max_seq_len, d) != ATTN_OK) return 0;
-  return plan_of(B, max_q, Hq, Hkv, max_seq_len, d).bytes;
+  // enough for either cache
+  const size_t x = plan_of(B, max_q, Hq, Hkv, max_seq_len, d, false).bytes;
+  const size_t y = plan_of(B, max_q, Hq, Hkv, max_seq_len, d, true).bytes;
+  return x > y ? x : y;
 }
 
 int attn_tree_paged(const void* q, const void* K_pages, const void* V_pages, const int32_t* block_table,

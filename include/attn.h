@@ -403,7 +403,7 @@ ATTN_API int attn_cache_read_e4m3(const void* K_codes, const void* V_codes, cons
  *   max_q      1 to 64.
  *   A token that sees no key gets 0.  Slots past len_b may hold anything.  A
  *   drafted key or value that is not finite reaches only the tokens that see
- *   it, whose output is then NaN.
+ *   it, which then holds NaN.
  *   ws         device workspace of attn_tree_workspace_bytes(...) bytes, 256-byte
  *              aligned; null where that is 0.  Its contents do not matter, and
  *              are not used by a later call.  Calls that may overlap on the GPU
