@@ -14,6 +14,7 @@ every query row's tile maximum is below its running maximum minus tau.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -177,32 +178,31 @@ def attn_decode_noalloc(q, K, V, o, B, Hq, Hkv, L, d, tau, stream=None, skip_mas
     return lib().attn_decode_noalloc(q, K, V, o, B, Hq, Hkv, L, d, float(tau), stream, skip_mask)
 
 
-_STRIDES = {n: ctypes.c_longlong * n for n in (6, 12)}
-
-
+@functools.lru_cache(maxsize=256)
 def _strides(values):
-    return _STRIDES[len(values)](*values)
+    """The C array of a tuple of strides (the library only reads it)."""
+    return (ctypes.c_longlong * len(values))(*values)
 
 
 def attn_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, B, N, Hq, Hkv, d, rot_dim,
                       interleaved, eps, strides, pos_stride_b, stream=None) -> int:
     """``strides``: 12 ints (batch, token and head stride of q, k, q_out, k_out, in elements)."""
     return lib().attn_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight, k_weight, B, N, Hq, Hkv, d,
-                                   rot_dim, int(interleaved), eps, _strides(strides), pos_stride_b, stream)
+                                   rot_dim, int(interleaved), eps, _strides(tuple(strides)), pos_stride_b, stream)
 
 
 def attn_cache_write_e4m3(k, v, slots, K_codes, V_codes, K_scales, V_scales, B, N, Hkv, num_pages, d, strides,
                           stream=None) -> int:
     """``strides``: 6 ints (batch, token and head stride of k and v, in elements)."""
     return lib().attn_cache_write_e4m3(k, v, slots, K_codes, V_codes, K_scales, V_scales, B, N, Hkv, num_pages,
-                                       d, _strides(strides), stream)
+                                       d, _strides(tuple(strides)), stream)
 
 
 def attn_cache_read_e4m3(K_codes, V_codes, K_scales, V_scales, slots, k, v, B, N, Hkv, num_pages, d, strides,
                          stream=None) -> int:
     """``strides``: 6 ints (batch, token and head stride of k and v, in elements)."""
     return lib().attn_cache_read_e4m3(K_codes, V_codes, K_scales, V_scales, slots, k, v, B, N, Hkv, num_pages,
-                                      d, _strides(strides), stream)
+                                      d, _strides(tuple(strides)), stream)
 
 
 def attn_tree_paged(q, K_pages, V_pages, block_table, seq_lens, cu_q, tree_mask, o, B, max_q, total_q, Hq, Hkv,
@@ -514,10 +514,8 @@ def _no(what: str, why: str) -> AttnError:
     return AttnError(1, f"{what} ({why})")
 
 
-def _device(what, tensors) -> int:
+def _device(what, tensors, torch) -> int:
     """The index of the tensors' one device, which is the current one (the library launches there)."""
-    import torch
-
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
@@ -529,26 +527,23 @@ def _device(what, tensors) -> int:
     return dev
 
 
-def _raw_stream(dev: int) -> int:
+def _raw_stream(dev: int, torch) -> int:
     """The current stream's cudaStream_t, without making a Stream object."""
-    import torch
-
     try:
         return torch._C._cuda_getCurrentRawStream(dev)
     except AttributeError:
         return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _run(dev, stream, tensors, make, call):
+def _run(dev, stream, tensors, make, call, torch):
     """call(make(), raw stream) on `stream` (None: the current one).  Memory that
     make() allocates belongs to that stream, and tensors that meet it from
     another one are recorded on it, so that the caching allocator keeps them
     until the call's kernels are done."""
-    import torch
-
-    if stream is None or stream.cuda_stream == _raw_stream(dev):
+    raw = _raw_stream(dev, torch)
+    if stream is None or stream.cuda_stream == raw:
         new = make()
-        return new, call(new, _raw_stream(dev))
+        return new, call(new, raw)
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
@@ -562,19 +557,13 @@ def _run(dev, stream, tensors, make, call):
     return new, call(new, stream.cuda_stream)
 
 
-def _contiguous_like(x):
-    import torch
-
-    return torch.empty_like(x, memory_format=torch.contiguous_format)
-
-
 def _token_strides(what, x):
     """(batch, token, head) strides of [tokens, H, d] or [B, H, N, d]; an axis of length 1 counts as 0."""
-    if x.dim() == 3:
-        (N, H, _), (sn, sh, sd) = x.shape, x.stride()
-        sb = 0
+    strides = x.stride()
+    if len(strides) == 3:
+        (N, H, _), (sn, sh, sd), sb = x.shape, strides, 0
     else:
-        (B, H, N, _), (sb, sh, sn, sd) = x.shape, x.stride()
+        (B, H, N, _), (sb, sh, sn, sd) = x.shape, strides
         if B == 1:
             sb = 0
     if sd != 1:
@@ -598,12 +587,14 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
 
     what = "qk_norm_rope"
     bf16 = torch.bfloat16
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
+    q_shape, k_shape = q.shape, k.shape
+    axes = len(q_shape)
+    if axes not in (3, 4) or len(k_shape) != axes:
         raise _no(what, "q and k must be [tokens, H, d] or [B, H, N, d]")
-    if q.dim() == 3:
-        (N, Hq, d), (Nk, Hkv, dk), B, Bk = q.shape, k.shape, 1, 1
+    if axes == 3:
+        (N, Hq, d), (Nk, Hkv, dk), B, Bk = q_shape, k_shape, 1, 1
     else:
-        (B, Hq, N, d), (Bk, Hkv, Nk, dk) = q.shape, k.shape
+        (B, Hq, N, d), (Bk, Hkv, Nk, dk) = q_shape, k_shape
     if N != Nk or d != dk or B != Bk:
         raise _no(what, "q and k must have the same tokens and head size")
     if q.dtype is not bf16 or k.dtype is not bf16:
@@ -611,16 +602,17 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     rot = pos_stride = 0
     pos_ptr = freq_ptr = None
     tensors = [q, k]
-    if inv_freq is not None and inv_freq.numel():
+    n_freq = 0 if inv_freq is None else inv_freq.numel()
+    if n_freq:
         if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous():
             raise _no(what, "inv_freq must be contiguous float32")
         shape = positions.shape
         if (positions.dtype is not torch.int32 or (N > 1 and positions.stride(-1) != 1) or
-                not (shape == (N,) or (q.dim() == 4 and shape == (B, N)))):
+                not (shape == (N,) or (axes == 4 and shape == (B, N)))):
             raise _no(what, "positions must be int32 [N] or [B, N]")
         if len(shape) == 2 and B > 1:
             pos_stride = positions.stride(0)
-        rot, pos_ptr, freq_ptr = 2 * inv_freq.numel(), positions.data_ptr(), inv_freq.data_ptr()
+        rot, pos_ptr, freq_ptr = 2 * n_freq, positions.data_ptr(), inv_freq.data_ptr()
         tensors += (positions, inv_freq)
     for w in (q_weight, k_weight):
         if w is not None:
@@ -628,43 +620,50 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
                 raise _no(what, "weights must be contiguous bf16 [d]")
             tensors.append(w)
     if out is not None:
-        if out[0].shape != q.shape or out[1].shape != k.shape or out[0].dtype is not bf16 or out[1].dtype is not bf16:
+        if out[0].shape != q_shape or out[1].shape != k_shape or out[0].dtype is not bf16 or out[1].dtype is not bf16:
             raise _no(what, "out must be bf16 of the inputs' shapes")
         tensors += out
     strides = _token_strides(what, q) + _token_strides(what, k)
-    out_strides = None if out is None else _token_strides(what, out[0]) + _token_strides(what, out[1])
-    dev = _device(what, tensors)
+    if out is not None:
+        strides += _token_strides(what, out[0]) + _token_strides(what, out[1])
+    elif axes == 3:  # contiguous ones; a stride of an axis of length 1 is not used
+        strides += (0, Hq * d, d, 0, Hkv * d, d)
+    else:
+        strides += (Hq * N * d, d, N * d, Hkv * N * d, d, N * d)
+    dev = _device(what, tensors, torch)
 
     def call(new, raw):
         qo, ko = new
-        so = out_strides or _token_strides(what, qo) + _token_strides(what, ko)
         return lib().attn_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), qo.data_ptr(), ko.data_ptr(), pos_ptr, freq_ptr,
             None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-            B, N, Hq, Hkv, d, rot, interleaved, eps, _strides(strides + so), pos_stride, raw)
+            B, N, Hq, Hkv, d, rot, interleaved, eps, _strides(strides), pos_stride, raw)
 
-    new, st = _run(dev, stream, tensors,
-                   lambda: out if out is not None else (_contiguous_like(q), _contiguous_like(k)), call)
+    def make():
+        if out is not None:
+            return out
+        form = torch.contiguous_format
+        return torch.empty_like(q, memory_format=form), torch.empty_like(k, memory_format=form)
+
+    new, st = _run(dev, stream, tensors, make, call, torch)
     if st:
         raise AttnError(st, "attn_qk_norm_rope")
     return new
 
 
-def _check_codes(what, K_codes, V_codes, K_scales, V_scales):
-    import torch
-
+def _check_codes(what, K_codes, V_codes, K_scales, V_scales, torch):
     shape = K_codes.shape
     if len(shape) != 4 or shape[2] != 64 or V_codes.shape != shape or K_codes.dtype is not torch.uint8 or \
             V_codes.dtype is not torch.uint8 or not K_codes.is_contiguous() or not V_codes.is_contiguous():
         raise _no(what, "codes must be contiguous uint8 [num_pages, Hkv, 64, d]")
-    if K_scales.shape != shape[:3] or V_scales.shape != shape[:3] or K_scales.dtype is not torch.float32 or \
+    groups = shape[:3]
+    if K_scales.shape != groups or V_scales.shape != groups or K_scales.dtype is not torch.float32 or \
             V_scales.dtype is not torch.float32 or not K_scales.is_contiguous() or not V_scales.is_contiguous():
         raise _no(what, "scales must be contiguous float32 [num_pages, Hkv, 64]")
+    return shape
 
 
-def _check_slots(what, slots):
-    import torch
-
+def _check_slots(what, slots, torch):
     if slots.dtype is not torch.int64 or slots.dim() not in (1, 2) or not slots.is_contiguous():
         raise _no(what, "slots must be contiguous int64, [tokens] or [B, N]")
 
@@ -681,28 +680,28 @@ def cache_write_e4m3(k, v, slots, K_codes, V_codes, K_scales, V_scales, stream=N
     import torch
 
     what = "cache_write_e4m3"
-    if k.dim() not in (3, 4) or k.shape != v.shape:
+    shape = k.shape
+    if len(shape) not in (3, 4) or v.shape != shape:
         raise _no(what, "k and v must be [tokens, H, d] or [B, H, N, d], of one shape")
     if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
         raise _no(what, "k and v must be bf16")
-    _check_codes(what, K_codes, V_codes, K_scales, V_scales)
-    _check_slots(what, slots)
-    if k.dim() == 3:
-        (N, Hkv, d), B, tokens = k.shape, 1, k.shape[:1]
+    pages, pool_heads, _, pool_d = _check_codes(what, K_codes, V_codes, K_scales, V_scales, torch)
+    _check_slots(what, slots, torch)
+    if len(shape) == 3:
+        (N, Hkv, d), B, tokens = shape, 1, shape[:1]
     else:
-        B, Hkv, N, d = k.shape
+        B, Hkv, N, d = shape
         tokens = (B, N)
-    pages, pool_heads, _, pool_d = K_codes.shape
     if pool_heads != Hkv or pool_d != d:
         raise _no(what, "the pool has other heads than k")
     if slots.shape != tokens:
         raise _no(what, "slots must have one entry a token")
     tensors = (k, v, slots, K_codes, V_codes, K_scales, V_scales)
-    dev = _device(what, tensors)
+    dev = _device(what, tensors, torch)
     strides = _strides(_token_strides(what, k) + _token_strides(what, v))
     _, st = _run(dev, stream, tensors, tuple, lambda _, raw: lib().attn_cache_write_e4m3(
         k.data_ptr(), v.data_ptr(), slots.data_ptr(), K_codes.data_ptr(), V_codes.data_ptr(), K_scales.data_ptr(),
-        V_scales.data_ptr(), B, N, Hkv, pages, d, strides, raw))
+        V_scales.data_ptr(), B, N, Hkv, pages, d, strides, raw), torch)
     if st:
         raise AttnError(st, "attn_cache_write_e4m3")
 
@@ -718,31 +717,35 @@ def cache_read_e4m3(K_codes, V_codes, K_scales, V_scales, slots, out=None, strea
 
     what = "cache_read_e4m3"
     bf16 = torch.bfloat16
-    _check_codes(what, K_codes, V_codes, K_scales, V_scales)
-    _check_slots(what, slots)
-    pages, Hkv, _, d = K_codes.shape
-    if slots.dim() == 1:
-        N, B = slots.shape[0], 1
+    pages, Hkv, _, d = _check_codes(what, K_codes, V_codes, K_scales, V_scales, torch)
+    _check_slots(what, slots, torch)
+    tokens = slots.shape
+    if len(tokens) == 1:
+        N, B = tokens[0], 1
         shape = (N, Hkv, d)
+        strides = (0, Hkv * d, d) * 2  # contiguous; a stride of an axis of length 1 is not used
     else:
-        B, N = slots.shape
+        B, N = tokens
         shape = (B, Hkv, N, d)
+        strides = (Hkv * N * d, d, N * d) * 2
     tensors = (K_codes, V_codes, K_scales, V_scales, slots)
     if out is not None:
         for t in out:
             if t.shape != shape or t.dtype is not bf16:
                 raise _no(what, "out must be bf16, [tokens, Hkv, d] or [B, Hkv, N, d] as slots are")
         tensors += tuple(out)
-        _token_strides(what, out[0]), _token_strides(what, out[1])
-    dev = _device(what, tensors)
+        strides = _token_strides(what, out[0]) + _token_strides(what, out[1])
+    dev = _device(what, tensors, torch)
 
     def make():
-        return out if out is not None else (K_scales.new_empty(shape, dtype=bf16), K_scales.new_empty(shape, dtype=bf16))
+        if out is not None:
+            return out
+        k = K_scales.new_empty(shape, dtype=bf16)
+        return k, torch.empty_like(k)
 
     new, st = _run(dev, stream, tensors, make, lambda new, raw: lib().attn_cache_read_e4m3(
         K_codes.data_ptr(), V_codes.data_ptr(), K_scales.data_ptr(), V_scales.data_ptr(), slots.data_ptr(),
-        new[0].data_ptr(), new[1].data_ptr(), B, N, Hkv, pages, d,
-        _strides(_token_strides(what, new[0]) + _token_strides(what, new[1])), raw))
+        new[0].data_ptr(), new[1].data_ptr(), B, N, Hkv, pages, d, _strides(strides), raw), torch)
     if st:
         raise AttnError(st, "attn_cache_read_e4m3")
     return new
@@ -773,7 +776,9 @@ def tree_paged(q, K_pages, V_pages, block_table, seq_lens, cu_q, max_q: int, max
 def tree_paged_e4m3(q, K_codes, V_codes, K_scales, V_scales, block_table, seq_lens, cu_q, max_q: int,
                     max_seq_len: int, tree_mask=None, out=None, stream=None, workspace=None):
     """tree_paged over the e4m3 cache that cache_write_e4m3 writes."""
-    _check_codes("tree_paged_e4m3", K_codes, V_codes, K_scales, V_scales)
+    import torch
+
+    _check_codes("tree_paged_e4m3", K_codes, V_codes, K_scales, V_scales, torch)
     return _tree("tree_paged_e4m3", q, K_codes, V_codes, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
                  max_seq_len, tree_mask, out, stream, workspace)
 
@@ -783,17 +788,18 @@ def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
     import torch
 
     bf16, int32 = torch.bfloat16, torch.int32
-    if q.dim() != 3 or q.dtype is not bf16 or not q.is_contiguous():
+    q_shape, pool, table = q.shape, K.shape, block_table.shape
+    if len(q_shape) != 3 or q.dtype is not bf16 or not q.is_contiguous():
         raise _no(what, "q must be contiguous bf16 [total_q, Hq, d]")
-    total, Hq, d = q.shape
-    if K.dim() != 4 or K.shape[2] != 64 or K.shape[3] != d:
+    total, Hq, d = q_shape
+    if len(pool) != 4 or pool[2] != 64 or pool[3] != d:
         raise _no(what, "the cache must be [num_pages, Hkv, 64, d]")
-    pages, Hkv = K.shape[:2]
+    pages, Hkv, _, _ = pool
     if block_table.dtype is not int32 or seq_lens.dtype is not int32 or cu_q.dtype is not int32 or \
             not block_table.is_contiguous() or not seq_lens.is_contiguous() or not cu_q.is_contiguous():
         raise _no(what, "block_table, seq_lens and cu_q must be contiguous int32")
     B = seq_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or cu_q.numel() != B + 1:
+    if len(table) != 2 or table[0] != B or cu_q.numel() != B + 1:
         raise _no(what, "block_table must be [B, max_pages] and cu_q [B + 1]")
     tensors = [q, K, V, block_table, seq_lens, cu_q]
     if K_scales is not None:
@@ -803,7 +809,7 @@ def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
             raise _no(what, "tree_mask must be contiguous int64 [total_q]")
         tensors.append(tree_mask)
     if out is not None:
-        if out.shape != q.shape or out.dtype is not bf16 or not out.is_contiguous():
+        if out.shape != q_shape or out.dtype is not bf16 or not out.is_contiguous():
             raise _no(what, "out must be contiguous bf16 of q's shape")
         tensors.append(out)
     need = 0
@@ -813,7 +819,7 @@ def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
         tensors.append(workspace)
     else:
         need = lib().attn_tree_workspace_bytes(B, max_q, total, Hq, Hkv, max_seq_len, d)
-    dev = _device(what, tensors)
+    dev = _device(what, tensors, torch)
 
     def make():
         return (torch.empty_like(q) if out is None else out,
@@ -826,14 +832,14 @@ def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
         if K_scales is None:
             return lib().attn_tree_paged(
                 q.data_ptr(), K.data_ptr(), V.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
-                mask, o.data_ptr(), B, max_q, total, Hq, Hkv, pages, block_table.shape[1], max_seq_len, d, raw, ws_ptr,
+                mask, o.data_ptr(), B, max_q, total, Hq, Hkv, pages, table[1], max_seq_len, d, raw, ws_ptr,
                 ws_bytes)
         return lib().attn_tree_paged_e4m3(
             q.data_ptr(), K.data_ptr(), V.data_ptr(), K_scales.data_ptr(), V_scales.data_ptr(), block_table.data_ptr(),
             seq_lens.data_ptr(), cu_q.data_ptr(), mask, o.data_ptr(), B, max_q, total, Hq, Hkv, pages,
-            block_table.shape[1], max_seq_len, d, raw, ws_ptr, ws_bytes)
+            table[1], max_seq_len, d, raw, ws_ptr, ws_bytes)
 
-    new, st = _run(dev, stream, tensors, make, call)
+    new, st = _run(dev, stream, tensors, make, call, torch)
     if st:
         raise AttnError(st, "attn_" + what)
     return new[0]
