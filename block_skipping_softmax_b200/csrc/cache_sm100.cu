@@ -43,25 +43,35 @@ struct CacheArgs {
 // A CTA takes neighbouring tokens of one head's keys or values, which are
 // neighbours in [B, H, N, d] and in a page; the CTAs of a token's other heads
 // run beside it, which are neighbours in a packed [tokens, H, d].
+// Finding a vector costs a dozen 64-bit operations, so lane c of a group finds
+// vector c % R for the others, and reads or writes its scale.
 struct Row {
-  bool valid;
-  long long x_at;  // element offset in x[side]
-  long long at;    // vector index in codes[side] and scales[side], -1 where the token has no slot
+  uint64_t x;    // address of the vector's first element in k or v, 0 past the last token
+  long long at;  // vector index in codes and scales, -1 where the token has no slot
 };
 
 __device__ __forceinline__ Row row_of(const CacheArgs& a, unsigned t, int side, int h) {
-  Row w;
-  w.valid = t < static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N);  // B * N < 2^31
-  w.x_at = 0;
-  w.at = -1;
-  if (w.valid) {
+  Row w{0, -1};
+  if (t < static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N)) {  // B * N < 2^31
     const unsigned b = a.B == 1 ? 0 : t / a.N, n = t - b * a.N;
     const long long slot = a.slots[t];
-    w.x_at = side ? b * a.xs[1][0] + n * a.xs[1][1] + h * a.xs[1][2]
-                  : b * a.xs[0][0] + n * a.xs[0][1] + h * a.xs[0][2];
+    const long long e = side ? b * a.xs[1][0] + n * a.xs[1][1] + h * a.xs[1][2]
+                             : b * a.xs[0][0] + n * a.xs[0][1] + h * a.xs[0][2];
+    w.x = reinterpret_cast<uint64_t>(side ? a.x[1] : a.x[0]) + 2 * e;
     if (slot >= 0 && slot < a.n_slots) w.at = ((slot / kPage) * a.Hkv + h) * kPage + slot % kPage;
   }
   return w;
+}
+
+template <int kLanes>
+__device__ __forceinline__ Row row_from(const Row& own, int r) {
+  return {__shfl_sync(kFull, own.x, r, kLanes), __shfl_sync(kFull, own.at, r, kLanes)};
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t m;  // a NaN stays
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(x), "r"(y));
+  return m;
 }
 
 template <int D, int R>
@@ -71,53 +81,69 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a
   const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
   const unsigned block = blockIdx.x / (2u * a.Hkv), head = blockIdx.x - block * (2u * a.Hkv);
   const int side = head >= static_cast<unsigned>(a.Hkv), h = side ? head - a.Hkv : head;
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(side ? a.x[1] : a.x[0]);
   uint8_t* codes = side ? a.codes[1] : a.codes[0];
   float* scales = side ? a.scales[1] : a.scales[0];
-  Row row[R];
+  const Row own = row_of(a, (block * R + c % R) * kGroups + group, side, h);
+  long long at[R];
   uint4 u[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    row[r] = row_of(a, (block * R + r) * kGroups + group, side, h);
+    const Row w = row_from<kLanes>(own, r);
+    at[r] = w.at;
     u[r] = make_uint4(0, 0, 0, 0);
-    if (row[r].at >= 0) u[r] = *reinterpret_cast<const uint4*>(x + row[r].x_at + c * 8);
+    if (at[r] >= 0) u[r] = reinterpret_cast<const uint4*>(w.x)[c];
   }
+  // max |x| of vector c % R: within the lane, then over the lanes; with four
+  // vectors a word carries two of them, and a lane ends with the pair of its own
+  uint32_t m[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    m[r] = max_bf16x2(max_bf16x2(u[r].x & kAbs, u[r].y & kAbs), max_bf16x2(u[r].z & kAbs, u[r].w & kAbs));
+  }
+  uint32_t top;
+  if constexpr (R == 4) {
+    const uint32_t p = max_bf16x2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+    const uint32_t q = max_bf16x2(__byte_perm(m[2], m[3], 0x5410), __byte_perm(m[2], m[3], 0x7632));
+    top = max_bf16x2(c & 2 ? q : p, __shfl_xor_sync(kFull, c & 2 ? p : q, 2));
+    top = max_bf16x2(top, __shfl_xor_sync(kFull, top, 1));
+  } else {
+    static_assert(R == 1, "one or four vectors");
+    top = max_bf16x2(m[0], __byte_perm(m[0], m[0], 0x1032));
+    top = max_bf16x2(top, __shfl_xor_sync(kFull, top, 1));
+    top = max_bf16x2(top, __shfl_xor_sync(kFull, top, 2));
+  }
+#pragma unroll
+  for (int o = 4; o < kLanes; o <<= 1) top = max_bf16x2(top, __shfl_xor_sync(kFull, top, o));
+  const uint32_t mx = R == 4 && !(c & 1) ? top << 16 : top & 0xffff0000u;  // as float bits
+  // mx = f 2^e with f in [1, 2); 448 = 1.75 * 2^8.  max|x| <= 448 * 2^k holds
+  // first at k = e - 8 when f <= 1.75, else at e - 7.  A subnormal mx (e field
+  // 0) lies below 448 * 2^-126, the least scale.  1/s is then exact too:
+  // |k| <= 126.
+  int k = static_cast<int>(mx >> 23) - 127 - 8 + ((mx & 0x7fffffu) > 0x600000u ? 1 : 0);
+  k = max(k, -126);
+  float s = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+  float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  if (mx == 0) s = inv = 1.f;
+  if (mx >= 0x7f800000u) s = inv = __uint_as_float(0x7fc00000u);  // inf or NaN in the vector
+  if (c < R && own.at >= 0) scales[own.at] = s;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float f = __shfl_sync(kFull, inv, r, kLanes);
     const uint32_t w[4] = {u[r].x, u[r].y, u[r].z, u[r].w};
-    uint32_t m = 0;  // max |x| as bits: non-negative floats order like their bits
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-    // m = f 2^e with f in [1, 2); 448 = 1.75 * 2^8.  max|x| <= 448 * 2^k holds
-    // first at k = e - 8 when f <= 1.75, else at e - 7.  A subnormal m (e field
-    // 0) lies below 448 * 2^-126, the least scale.  1/s is then exact too:
-    // |k| <= 126.
-    int k = static_cast<int>(m >> 23) - 127 - 8 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
-    k = max(k, -126);
-    float s = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-    float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-    if (m == 0) s = inv = 1.f;
-    if (m >= 0x7f800000u) s = inv = __uint_as_float(0x7fc00000u);  // inf or NaN in the vector
     uint32_t out[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint16_t lo, hi;  // cvt packs its first source into the upper byte
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
           : "=h"(lo)
-          : "f"(__uint_as_float(w[2 * i] & 0xffff0000u) * inv),
-            "f"(__uint_as_float(w[2 * i] << 16) * inv));
+          : "f"(__uint_as_float(w[2 * i] & 0xffff0000u) * f), "f"(__uint_as_float(w[2 * i] << 16) * f));
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
           : "=h"(hi)
-          : "f"(__uint_as_float(w[2 * i + 1] & 0xffff0000u) * inv),
-            "f"(__uint_as_float(w[2 * i + 1] << 16) * inv));
+          : "f"(__uint_as_float(w[2 * i + 1] & 0xffff0000u) * f), "f"(__uint_as_float(w[2 * i + 1] << 16) * f));
       out[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
     }
-    if (row[r].at >= 0) {
-      *reinterpret_cast<uint2*>(codes + row[r].at * D + c * 8) = make_uint2(out[0], out[1]);
-      if (c == 0) scales[row[r].at] = s;
-    }
+    if (at[r] >= 0) *reinterpret_cast<uint2*>(codes + at[r] * D + c * 8) = make_uint2(out[0], out[1]);
   }
 }
 
@@ -128,24 +154,22 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a)
   const int group = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
   const unsigned block = blockIdx.x / (2u * a.Hkv), head = blockIdx.x - block * (2u * a.Hkv);
   const int side = head >= static_cast<unsigned>(a.Hkv), h = side ? head - a.Hkv : head;
-  __nv_bfloat16* x = static_cast<__nv_bfloat16*>(const_cast<void*>(side ? a.x[1] : a.x[0]));
   const uint8_t* codes = side ? a.codes[1] : a.codes[0];
   const float* scales = side ? a.scales[1] : a.scales[0];
-  Row row[R];
+  const Row own = row_of(a, (block * R + c % R) * kGroups + group, side, h);
+  const float s = own.at >= 0 ? scales[own.at] : 0.f;
+  uint64_t x[R];
   uint2 u[R];
-  float s[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    row[r] = row_of(a, (block * R + r) * kGroups + group, side, h);
+    const Row w = row_from<kLanes>(own, r);
+    x[r] = w.x;
     u[r] = make_uint2(0, 0);
-    s[r] = 0.f;
-    if (row[r].at >= 0) {
-      u[r] = *reinterpret_cast<const uint2*>(codes + row[r].at * D + c * 8);
-      s[r] = scales[row[r].at];
-    }
+    if (w.at >= 0) u[r] = *reinterpret_cast<const uint2*>(codes + w.at * D + c * 8);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
+    const float f = __shfl_sync(kFull, s, r, kLanes);
     uint32_t out[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -153,10 +177,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a)
       uint32_t h2;  // two halves: every e4m3 value is exact in fp16
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(pair)));
       const __half2 h = *reinterpret_cast<const __half2*>(&h2);
-      out[i] = pack_bf16x2(__low2float(h) * s[r], __high2float(h) * s[r]);
+      out[i] = pack_bf16x2(__low2float(h) * f, __high2float(h) * f);
     }
-    if (row[r].valid)
-      *reinterpret_cast<uint4*>(x + row[r].x_at + c * 8) = make_uint4(out[0], out[1], out[2], out[3]);
+    if (x[r]) reinterpret_cast<uint4*>(x[r])[c] = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
