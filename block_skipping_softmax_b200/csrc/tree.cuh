@@ -38,16 +38,13 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 }
 
 // mbar_wait in fewer instructions, for kernels whose roles wait in many places:
-// one poll, and a look at the flag and the clock every 64.  NAP: between polls
-// the warp sleeps, and leaves the issue slots to the warps that work.
-template <int NAP = 0>
+// one poll, and a look at the flag and the clock every 64.
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
                                           uint64_t limit_ns) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if constexpr (NAP > 0) __nanosleep(NAP);
     if ((i & 63u) == 0) {
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;

@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           }
         }
       }
-      __syncwarp();  // every lane has read the slot
+      fence_proxy_async_smem();  // the reads of the slot stay before the copy that overwrites it
+      __syncwarp();
       if (i + C::kStages < mine) issue(i + C::kStages, s);
     }
 

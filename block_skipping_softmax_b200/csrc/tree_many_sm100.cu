@@ -449,17 +449,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           bad &= sees;
         }
         const bool plain = !E4M3 || plain_tile(n);
-        // an unusual e4m3 tile: 16 columns at a time, with their scales and mask
-        auto scaled16 = [&](int c0, uint32_t (&y)[16]) {
-          tmem_ld16(tS(sb) + lane_off + c0, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float ks = lds_f32(sbase + C::kOffKScale + ((n & 3) * kPage + c0 + c) * 4);
-            y[c] = __float_as_uint(__uint_as_float(y[c]) * ks);
-            if (!((sees >> (c0 + c)) & 1)) y[c] = 0xff800000u;
-          }
-        };
         // the tile's maximum to the running reference; moves O along, and gives
         // the value that the exponents are relative to
         float alpha = 1.f, base = 0.f, rs = 0.f;
