@@ -108,6 +108,15 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 constexpr int kPShift = 7;
 __device__ __forceinline__ bool fits_f16(float scale) { return scale >= pow2(-15) && scale <= pow2(7); }
 
+// The exponents of two probabilities: (score - reference) * scale, in log2 units.
+// minus(reference) is 0 where nothing has been seen so far: then all p are 0.
+__device__ __forceinline__ float minus(float ref) { return ref == neg_inf() ? 0.f : -ref; }
+template <bool SHIFT>
+__device__ __forceinline__ float2 log2_p(float2 score, float2 from, float2 by) {
+  const float2 x = __fadd2_rn(score, from);
+  return SHIFT ? __ffma2_rn(x, by, make_float2(kPShift, kPShift)) : __fmul2_rn(x, by);
+}
+
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));

@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         for (int c = 0; c < 2; ++c) {
           float m = fmaxf(sc[0][t][c], sc[0][t][2 + c]);
           if constexpr (KB == 2) m = fmax3(m, sc[1][t][c], sc[1][t][2 + c]);
-          mt[t][c] = m * mul[t][c];
-          move |= mt[t][c] > ref[t][c] + kRefSlack;
+          mt[t][c] = m;
+          move |= (m - ref[t][c]) * mul[t][c] > kRefSlack;  // NaN where nothing has been seen still
         }
       if (__any_sync(kFull, move)) {
 #pragma unroll
@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             float m = mt[t][c];
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
-            const float to = m > ref[t][c] + kRefSlack ? m : ref[t][c];
-            const float al = to == ref[t][c] ? 1.f : ex2(ref[t][c] - to);  // ref = -inf gives 0
+            const float to = (m - ref[t][c]) * mul[t][c] > kRefSlack ? m : ref[t][c];
+            const float al = to == ref[t][c] ? 1.f : ex2((ref[t][c] - to) * mul[t][c]);  // ref = -inf gives 0
             ref[t][c] = to;
             sum[t][c] *= al;
 #pragma unroll
@@ -402,21 +402,20 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             for (int e = 0; e < 4; ++e) vs[b][e] = 0.f;
         }
       }
-      // ---- P^T as the B operand.  As bf16, the sums adding the rounded values
+      // ---- P^T as the B operand, of 2^((s - ref) scale): the difference first, which
+      // keeps its bits at any size of the scores.  As bf16, the sums adding the rounded values
       // that the product meets; as fp16, whose rounding (2^-12) is below what
       // cancels there.
       uint32_t pb[KB][NT][2];  // rows 8 t + n; keys key_lo, + kStep (0) and 8 further (1)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float base[2];  // nothing seen so far: all p are 0
-#pragma unroll
-        for (int c = 0; c < 2; ++c) base[c] = ref[t][c] == neg_inf() ? 0.f : ref[t][c] - (E4M3 ? kPShift : 0);
+        const float2 from = make_float2(minus(ref[t][0]), minus(ref[t][1])), by = make_float2(mul[t][0], mul[t][1]);
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2(fmaf(sc[b][t][2 * h], mul[t][0], -base[0]));
-            const float p1 = ex2(fmaf(sc[b][t][2 * h + 1], mul[t][1], -base[1]));
+            const float2 x = log2_p<E4M3>(make_float2(sc[b][t][2 * h], sc[b][t][2 * h + 1]), from, by);
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
             uint32_t w;
             if (f16) {
               w = pack_f16x2(p0, p1);
@@ -590,9 +589,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float x = wmax[w * kRows + r];
-          den[t][c] += (x == M[t][c] ? 1.f : ex2(x - M[t][c])) * wsum[w * kRows + r];
+          den[t][c] += (x == M[t][c] ? 1.f : ex2((x - M[t][c]) * mul[t][c])) * wsum[w * kRows + r];
         }
-        const float f = ref[t][c] == M[t][c] ? 1.f : ex2(ref[t][c] - M[t][c]);
+        const float f = ref[t][c] == M[t][c] ? 1.f : ex2((ref[t][c] - M[t][c]) * mul[t][c]);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           o[j][t][c] *= f;
@@ -626,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           const size_t share = share_at(a, kRows, blockIdx.y, blockIdx.x, sg.place, r);
           const size_t at = row_at(a, sg, r);
           if (!sg.whole && n == 0)
-            a.lse[share] = empty ? neg_inf() : M[t][c] + __log2f(den[t][c]) - (E4M3 ? kPShift : 0);
+            a.lse[share] = empty ? neg_inf() : M[t][c] * mul[t][c] + __log2f(den[t][c]) - (E4M3 ? kPShift : 0);
           // this lane's columns, in runs of 8: block pair j holds columns
           // 2j and 2j + 1 of the lane's chunk of 16 codes, or of 8 values a panel
 #pragma unroll

@@ -451,15 +451,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
         const bool plain = !E4M3 || plain_tile(n);
         // the tile's maximum to the running reference; moves O along, and gives
         // the value that the exponents are relative to
-        float alpha = 1.f, base = 0.f, rs = 0.f;
+        float alpha = 1.f, from = 0.f, rs = 0.f;
         auto refer = [&](float mt) {
-          mt *= mul;
-          const bool moved = mt > m_ref + kRefSlack;
+          const bool moved = (mt - m_ref) * mul > kRefSlack;  // NaN where nothing has been seen still
           if (moved) {
-            alpha = ex2(m_ref - mt);  // m_ref = -inf gives 0
+            alpha = ex2((m_ref - mt) * mul);  // m_ref = -inf gives 0
             m_ref = mt;
           }
-          base = m_ref == neg_inf() ? 0.f : m_ref - (E4M3 ? kPShift : 0);
+          from = minus(m_ref);
           if (__any_sync(kFull, moved && j > 0)) {
             // O is read and written back: the last P V must have finished
             if (!__all_sync(kFull, mbar_poll(b_pv_done, (n - 1) & 1, abort_flag, a.wait_limit_ns))) {
@@ -479,7 +478,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           }
           return true;
         };
-        // P = 2^(x - ref) over the scores: as bf16, the sum adding the rounded
+        // P = 2^((s - ref) scale), the difference first, which keeps its bits at any
+        // size of the scores: as bf16, the sum adding the rounded
         // values; as fp16, whose rounding (2^-12) is below what cancels there
         if (plain) {
           uint32_t x[kPage];
@@ -497,27 +497,27 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
             for (int e = 0; e < 4; ++e)
               mt[e] = fmax3(mt[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
           if (!(ok = refer(fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]))))) break;
-          float rs2 = 0.f;
+          const float2 from2 = make_float2(from, from), mul2 = make_float2(mul, mul);
+          float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c0 = 0; c0 < kPage; c0 += 32) {
             uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const float p0 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c]), mul, -base));
-              const float p1 = ex2(fmaf(__uint_as_float(x[c0 + 2 * c + 1]), mul, -base));
+              const float2 y = log2_p<E4M3>(
+                  make_float2(__uint_as_float(x[c0 + 2 * c]), __uint_as_float(x[c0 + 2 * c + 1])), from2, mul2);
+              const float p0 = ex2(y.x), p1 = ex2(y.y);
               if constexpr (E4M3) {
                 pk[c] = pack_f16x2(p0, p1);
-                rs += p0;
-                rs2 += p1;
+                sum2 = __fadd2_rn(sum2, make_float2(p0, p1));
               } else {
                 pk[c] = pack_bf16x2(p0, p1);
-                rs += __uint_as_float(pk[c] << 16);
-                rs2 += __uint_as_float(pk[c] & 0xffff0000u);
+                sum2 = __fadd2_rn(sum2, make_float2(__uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xffff0000u)));
               }
             }
             tmem_st16(tS(sb) + lane_off + c0 / 2, pk);
           }
-          rs += rs2;
+          rs = sum2.x + sum2.y;
         } else {  // an unusual e4m3 tile: 16 columns at a time, with their scales and mask
           auto scaled16 = [&](int c0, uint32_t (&y)[16]) {
             tmem_ld16(tS(sb) + lane_off + c0, y);
@@ -544,8 +544,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
             scaled16(c0, y);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              pk[c] = pack_bf16x2(ex2(fmaf(__uint_as_float(y[2 * c]), mul, -base)),
-                                  ex2(fmaf(__uint_as_float(y[2 * c + 1]), mul, -base)));
+              const float2 z = log2_p<E4M3>(make_float2(__uint_as_float(y[2 * c]), __uint_as_float(y[2 * c + 1])),
+                                            make_float2(from, from), make_float2(mul, mul));
+              pk[c] = pack_bf16x2(ex2(z.x), ex2(z.y));
               rs += __uint_as_float(pk[c] << 16) + __uint_as_float(pk[c] & 0xffff0000u);
             }
             tmem_st8(tS(sb) + lane_off + c0 / 2, pk);
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
         const bool empty = l_sum == 0.f;  // a row that sees nothing here
         const float inv = empty ? 0.f : 1.f / l_sum;
         const size_t share = share_at(a, kRows, blockIdx.y, blockIdx.x, sg.place, r);
-        if (valid && !sg.whole) a.lse[share] = empty ? neg_inf() : m_ref + __log2f(l_sum) - (E4M3 ? kPShift : 0);
+        if (valid && !sg.whole) a.lse[share] = empty ? neg_inf() : m_ref * mul + __log2f(l_sum) - (E4M3 ? kPShift : 0);
         float* part = a.part + share * D;
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + at * D;
 #pragma unroll 1
