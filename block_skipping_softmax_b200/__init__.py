@@ -783,6 +783,11 @@ def tree_paged_e4m3(q, K_codes, V_codes, K_scales, V_scales, block_table, seq_le
                  max_seq_len, tree_mask, out, stream, workspace)
 
 
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(*sizes) -> int:
+    return lib().attn_tree_workspace_bytes(*sizes)
+
+
 def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q, max_seq_len, tree_mask, out,
           stream, workspace):
     import torch
@@ -818,7 +823,7 @@ def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
             raise _no(what, "workspace must be contiguous uint8")
         tensors.append(workspace)
     else:
-        need = lib().attn_tree_workspace_bytes(B, max_q, total, Hq, Hkv, max_seq_len, d)
+        need = _tree_workspace(B, max_q, total, Hq, Hkv, max_seq_len, d)
     dev = _device(what, tensors, torch)
 
     def make():
