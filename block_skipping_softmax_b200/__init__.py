@@ -522,7 +522,11 @@ def _device(what, tensors, torch) -> int:
             raise _no(what, "tensors must be on one CUDA device")
     if dev < 0:
         raise _no(what, "tensors must be CUDA tensors")
-    if dev != torch.cuda.current_device():
+    try:
+        current = torch._C._cuda_getDevice()  # CUDA is up: there are tensors on it
+    except AttributeError:
+        current = torch.cuda.current_device()
+    if dev != current:
         raise _no(what, "tensors must be on the current CUDA device")
     return dev
 
