@@ -18,6 +18,10 @@
 // chunk of its angles, and loads a row ahead of the one that it turns.  The
 // tokens' sines and cosines are made once, into shared memory, while the first
 // rows are on their way.
+//
+// 8192 tokens x 40 heads of 128: 29.7 us, 5.7 TB/s of the 6.55 of a copy; 30011
+// x 20 heads of 64: 29.9 us, 5.1 TB/s, with a third of the issue slots idle and
+// about 40 KB in flight an SM.  Two values to an fp32 instruction changed nothing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -179,10 +183,13 @@ void launch_d(RopeArgs& a, cudaStream_t s) {
   a.groups = kGroups;
   a.heads = a.H;
   if (static_cast<long long>(tokens) * passes <= 148 * 6) {
-    // all rows at once: the latency of a call is one row's
+    // all rows at once: the latency of a call is one row's (16 tokens x 40 heads of
+    // 128: 3.1 us, 5.9 by the rule below)
     a.heads = kGroups;
   } else {
-    // the most groups a token that leave at most a tenth of them idle
+    // the most groups a token that leave at most a tenth of them idle (with one
+    // token a CTA, 8192 x 40 heads take 39.9 us instead of 29.7, 30011 x 20 heads
+    // of 64 110 instead of 29.9)
     auto idle = [&](int g) { return 10 * (((a.H + g - 1) / g) * g - a.H) > ((a.H + g - 1) / g) * g; };
     while (a.groups > 1 && idle(a.groups)) a.groups /= 2;
   }

@@ -150,7 +150,8 @@ __device__ __forceinline__ Seq seq_of(const TreeLaunch& a, int b) {
 // A segment has its own start and end (queries, first copies, adding up the
 // warps' sums), worth about kSegment tiles, and a piece has two of them mostly.  So
 // heads are kept whole unless their longest share is longer than an equal piece
-// by more than that.
+// by more than that.  (One token over 8192 keys takes 13.5 us so, 18 with 0 or
+// with 64 in its place; 37 sequences over 4096 keys 62, 62 and 59.)
 //
 // A segment that is not all of its KV head's tiles leaves a share of the result
 // in one of the CTA's two places (only its first and its last segment can be
