@@ -28,20 +28,22 @@ namespace bss {
 
 namespace {
 
-// The sum of the shares of a KV head's keys, exact up to fp32.  W warps take a
-// row, each every W-th share; a lane holds D/32 columns.  Rows that one CTA has
-// finished are left alone.  The kernel starts while the one before it ends,
-// and looks for its shares meanwhile.
-template <int D, int W>
+constexpr int kFew = 4;  // shares whose loads a warp issues at once
+
+// The sum of the shares of a KV head's keys, exact up to fp32.  A warp takes R
+// rows of a KV head, or W warps take one, each every W-th share; a lane holds D/32
+// columns.  Rows that one CTA has finished are left alone.  The kernel starts
+// while the one before it ends, and looks for its shares meanwhile.
+template <int D, int W, int R>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__ TreeLaunch a, int per) {
-  static_assert(W == 1 || W == 4, "a row's warps are in one CTA");
+  static_assert((W == 1 || W == 4) && (W == 1 || R == 1) && 8 % R == 0, "a row's warps are in one CTA");
   const int b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
   const Seq s = seq_of(a, b);
-  const int r = blockIdx.x * (4 / W) + warp / W;
-  const int group = a.Hq / a.Hkv, head = r % a.Hq;
-  const int kv = head / group, row = (r / a.Hq) * group + head % group;  // row of the KV head
-  const int plane = row / per;
+  const int group = a.Hq / a.Hkv;
+  const int units = (a.max_q * group + R - 1) / R;  // of a KV head
+  const int unit = blockIdx.x * (4 / W) + warp / W, kv = unit / units, row0 = (unit - kv * units) * R;
+  const int plane = row0 / per;  // of all R rows: per is a multiple of 8
   // this KV head's shares: CTAs c0 to c1, of which the first may be in the CTA's
   // second place
   Line line;
@@ -50,7 +52,8 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   const int span = max(1, (s.len + kPage - 1) / kPage);
   const int head_at = line.heads_at(a, b - line.chunk) + kv;
   const int first = line.before + __shfl_sync(kFull, line.incl - line.tiles * a.Hkv, b - line.chunk) + kv * span;
-  if (r >= s.T * a.Hq) return;  // the same for all warps of a row
+  const int rows = min(s.T * group, row0 + R);
+  if (kv >= a.Hkv || row0 >= rows) return;  // the same for all warps of a row
   int c0, c1, place0 = 0;
   if (div.shares) {
     c0 = head_at * div.shares;
@@ -66,74 +69,119 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
     const long long i = c - c0;
     return div.shares > span && span * i / div.shares == span * (i + 1) / div.shares;
   };
-  auto share = [&](int c) { return share_at(a, per, plane, c, c == c0 ? place0 : 0, row - plane * per); };
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float M = neg_inf();
-  for (int c = c0 + lane; c <= c1; c += 32)
-    if (!empty(c)) M = fmaxf(M, a.lse[share(c)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
   constexpr int kC = D / 32;
-  float num[kC], den = 0.f;
+  auto write = [&](int row, const float (&num)[kC], float den) {
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const size_t at = static_cast<size_t>(s.tok0 + row / group) * a.Hq + kv * group + row % group;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + at * D + lane * kC;
 #pragma unroll
-  for (int c = 0; c < kC; ++c) num[c] = 0.f;
-  for (int base = c0 + part; base <= c1; base += 32 * W) {
-    // lane i: weight of share base + i W
-    float w = 0.f;
-    if (base + lane * W <= c1 && !empty(base + lane * W)) {
-      const float l = a.lse[share(base + lane * W)];
-      w = l == neg_inf() ? 0.f : l == M ? 1.f : ex2(l - M);  // 0: nothing seen there
+    for (int e = 0; e < kC; e += 2)
+      *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(num[e] * inv, num[e + 1] * inv);
+  };
+  if (R > 1 && c1 - c0 < kFew) {  // all loads of two rows at once
+#pragma unroll 2
+    for (int row = row0; row < rows; ++row) {
+      float l[kFew], M = neg_inf(), den = 0.f, num[kC];
+      float2 v[kFew][kC / 2];
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        const int c = min(c0 + i, c1);
+        const size_t at = share_at(a, per, plane, c, c == c0 ? place0 : 0, row - plane * per);
+        l[i] = c0 + i > c1 || empty(c) ? neg_inf() : a.lse[at];
+#pragma unroll
+        for (int e = 0; e < kC / 2; ++e) v[i][e] = reinterpret_cast<const float2*>(a.part + at * D + lane * kC)[e];
+      }
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) M = fmaxf(M, l[i]);
+#pragma unroll
+      for (int e = 0; e < kC; ++e) num[e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        // 0: nothing seen there, and its sums perhaps not written
+        const float w = l[i] == neg_inf() ? 0.f : l[i] == M ? 1.f : ex2(l[i] - M);
+        den += w;
+        if (w != 0.f) {
+#pragma unroll
+          for (int e = 0; e < kC / 2; ++e) {
+            num[2 * e] = fmaf(w, v[i][e].x, num[2 * e]);
+            num[2 * e + 1] = fmaf(w, v[i][e].y, num[2 * e + 1]);
+          }
+        }
+      }
+      write(row, num, den);
     }
-    den += w;
-    const int n = min(32, (c1 - base) / W + 1);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(kFull, w, i);
-      if (wi == 0.f) continue;  // an empty share, perhaps: its sums were not written
-      const float* x = a.part + share(base + i * W) * D + lane * kC;
+    return;
+  }
+#pragma unroll 1
+  for (int row = row0; row < rows; ++row) {
+    auto share = [&](int c) { return share_at(a, per, plane, c, c == c0 ? place0 : 0, row - plane * per); };
+    float M = neg_inf();
+    for (int c = c0 + lane; c <= c1; c += 32)
+      if (!empty(c)) M = fmaxf(M, a.lse[share(c)]);
 #pragma unroll
-      for (int e = 0; e < kC; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(x + e);
-        num[e] = fmaf(wi, v.x, num[e]);
-        num[e + 1] = fmaf(wi, v.y, num[e + 1]);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float num[kC], den = 0.f;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) num[c] = 0.f;
+    for (int base = c0 + part; base <= c1; base += 32 * W) {
+      // lane i: weight of share base + i W
+      float w = 0.f;
+      if (base + lane * W <= c1 && !empty(base + lane * W)) {
+        const float l = a.lse[share(base + lane * W)];
+        w = l == neg_inf() ? 0.f : l == M ? 1.f : ex2(l - M);  // 0: nothing seen there
+      }
+      den += w;
+      const int n = min(32, (c1 - base) / W + 1);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float* x = a.part + share(base + i * W) * D + lane * kC;
+        float2 v[kC / 2];
+#pragma unroll
+        for (int e = 0; e < kC / 2; ++e) v[e] = reinterpret_cast<const float2*>(x)[e];
+        const float wi = __shfl_sync(kFull, w, i);
+        if (wi != 0.f) {  // else an empty share, perhaps: its sums were not written
+#pragma unroll
+          for (int e = 0; e < kC / 2; ++e) {
+            num[2 * e] = fmaf(wi, v[e].x, num[2 * e]);
+            num[2 * e + 1] = fmaf(wi, v[e].y, num[2 * e + 1]);
+          }
+        }
       }
     }
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
-  if constexpr (W > 1) {
-    __shared__ float red[W][D + 1];
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
+    if constexpr (W > 1) {
+      __shared__ float red[W][D + 1];
 #pragma unroll
-    for (int e = 0; e < kC; ++e) red[part][lane * kC + e] = num[e];
-    if (lane == 0) red[part][D] = den;
-    __syncthreads();
-    if (part != 0) return;
+      for (int e = 0; e < kC; ++e) red[part][lane * kC + e] = num[e];
+      if (lane == 0) red[part][D] = den;
+      __syncthreads();
+      if (part != 0) return;
 #pragma unroll
-    for (int x = 1; x < W; ++x) {
-      den += red[x][D];
+      for (int x = 1; x < W; ++x) {
+        den += red[x][D];
 #pragma unroll
-      for (int e = 0; e < kC; ++e) num[e] += red[x][lane * kC + e];
+        for (int e = 0; e < kC; ++e) num[e] += red[x][lane * kC + e];
+      }
     }
+    write(row, num, den);
   }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (static_cast<size_t>(s.tok0) * a.Hq + r) * D + lane * kC;
-#pragma unroll
-  for (int e = 0; e < kC; e += 2)
-    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(num[e] * inv, num[e + 1] * inv);
 }
 
-template <int D, int W>
+template <int D, int W, int R>
 int launch_merge(const TreeLaunch& a, int per) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((a.max_q * a.Hq + 4 / W - 1) / (4 / W), a.B);
+  const int group = a.Hq / a.Hkv, units = (a.max_q * group + R - 1) / R * a.Hkv;
+  cfg.gridDim = dim3((units + 4 / W - 1) / (4 / W), a.B);
   cfg.blockDim = dim3(128);
   cfg.stream = a.stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, W>, a, per) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, W, R>, a, per) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // The launch, as far as the sizes decide it.
@@ -186,6 +234,16 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
   return p;
 }
 
+// Four warps a row where a KV head has many shares; four rows a warp where there are
+// more than the SMs hold warps for at once (16384 rows of 3 shares each, from HBM:
+// 15.4 us, 19.6 by one row a warp, whose way to its shares then costs most).
+template <int D>
+int merge(const TreeLaunch& a, const Plan& p) {
+  if (p.ctas > 8ll * a.B * a.Hkv) return launch_merge<D, 4, 1>(a, p.per);
+  if (static_cast<long long>(a.B) * a.max_q * a.Hq > 148 * 16) return launch_merge<D, 1, 4>(a, p.per);
+  return launch_merge<D, 1, 1>(a, p.per);
+}
+
 int check_sizes(int B, int max_q, int total_q, int Hq, int Hkv, int L, int d) {
   if (B <= 0 || max_q <= 0 || max_q > 64 || total_q <= 0 || Hq <= 0 || Hkv <= 0 || L <= 0)
     return ATTN_ERR_INVALID_ARG;
@@ -224,10 +282,7 @@ int run_tree(TreeLaunch& a, void* ws, size_t ws_bytes, void* stream) {
   a.stream = static_cast<cudaStream_t>(stream);
   st = p.per < kManyRows ? launch_tree_few(a, p.per) : launch_tree_many(a);
   if (st != ATTN_OK || !p.shares) return st;
-  // four warps a row where a KV head has many shares
-  const bool many = p.ctas > 8ll * a.B * a.Hkv;
-  if (a.d == 64) return many ? launch_merge<64, 4>(a, p.per) : launch_merge<64, 1>(a, p.per);
-  return many ? launch_merge<128, 4>(a, p.per) : launch_merge<128, 1>(a, p.per);
+  return a.d == 64 ? merge<64>(a, p) : merge<128>(a, p);
 }
 
 }  // namespace
