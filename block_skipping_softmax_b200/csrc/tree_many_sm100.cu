@@ -23,7 +23,7 @@
 //   bf16 of 128  168 / 184 / 206 us   of 64  102 / 124 / 148
 //   e4m3 of 128  186 / 207 / 239      of 64  139 (32 rows) / 168 / 200
 // bf16 is bound by HBM up to 64 rows (6.3 TB/s).  With 512 rows a head (64 tokens x
-// 64 heads over 4 x 16384 keys: 199 us, 690 TFLOP/s) the tensor pipe, the ex2 unit
+// 64 heads over 4 x 16384 keys: 195 us with the merge, 704 TFLOP/s) the tensor pipe, the ex2 unit
 // and the issue slots are each busy for 46 to 49% of the time: what counts is the
 // latency of S, softmax and P, with two warps a scheduler to hide it.  e4m3 adds
 // the latency of the conversion, and more warps to the same schedulers.  Slower:
