@@ -53,6 +53,9 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   const int head_at = line.heads_at(a, b - line.chunk) + kv;
   const int first = line.before + __shfl_sync(kFull, line.incl - line.tiles * a.Hkv, b - line.chunk) + kv * span;
   const int rows = min(s.T * group, row0 + R);
+  // Every CTA waits here, those without work too: what follows in the stream may
+  // count on this kernel's end alone.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (kv >= a.Hkv || row0 >= rows) return;  // the same for all warps of a row
   int c0, c1, place0 = 0;
   if (div.shares) {
@@ -69,7 +72,6 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
     const long long i = c - c0;
     return div.shares > span && span * i / div.shares == span * (i + 1) / div.shares;
   };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kC = D / 32;
   auto write = [&](int row, const float (&num)[kC], float den) {
     const float inv = den == 0.f ? 0.f : 1.f / den;

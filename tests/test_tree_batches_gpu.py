@@ -160,3 +160,20 @@ def test_the_same_call_gives_the_same_bits(cache, T, g):
     for _ in range(20):
         assert torch.equal(c.run().view(torch.int16), first.view(torch.int16))
     check(c, first)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("T,g", [(1, 4), (9, 8)])
+def test_what_follows_in_the_stream_sees_the_result(cache, T, g):
+    """Heads that one CTA finishes leave the merge nothing to do; a copy behind it still waits for them."""
+    c = Case(cache, [800] * 37, [T] * 37, 8 * g, 8, 128, seed=T)
+    first = c.run()
+    out = torch.empty_like(first)
+    copies = []
+    for _ in range(30):
+        out.fill_(NAN)
+        c.run(out=out)
+        copies.append(out.clone())
+    rows = slice(0, c.starts[-1])
+    assert all(torch.equal(x[rows], first[rows]) for x in copies)
+    check(c, first)
