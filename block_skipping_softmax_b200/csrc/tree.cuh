@@ -144,13 +144,15 @@ __device__ __forceinline__ Seq seq_of(const TreeLaunch& a, int b) {
 // the line of all its tiles: sequences, KV heads and tiles, in this order.  It
 // is divided among the plane's CTAs in one of two ways.
 //   By heads: every KV head's tiles go to `shares` CTAs of their own.
-//   Equal pieces: the line is cut into pieces that differ by one tile at most,
-//   whatever the sequences' lengths, so a ragged batch keeps every SM busy to
-//   the end.  A piece consists of segments, runs of tiles of one KV head.
+//   Equal pieces: the line is cut into pieces of the same cost, whatever the
+//   sequences' lengths, so a ragged batch keeps every SM busy to the end.  A
+//   piece consists of segments, runs of tiles of one KV head.
 // A segment has its own start and end (queries, first copies, adding up the
-// warps' sums), worth about kSegment tiles, and a piece has two of them mostly.  So
-// heads are kept whole unless their longest share is longer than an equal piece
-// by more than that.  (One token over 8192 keys takes 13.5 us so, 18 with 0 or
+// warps' sums), worth about kSegment tiles: every KV head has as many places on
+// the line more than tiles, behind them, so that a piece across a head's end has
+// fewer tiles.  (By tiles alone the CTAs with two segments ended 4 to 12 us behind the
+// others.)  Heads are kept whole where their longest share is no longer than an
+// equal piece.  (One token over 8192 keys takes 13.5 us so, 18 with 0 or
 // with 64 in its place; 37 sequences over 4096 keys 62, 62 and 59.)
 //
 // A segment that is not all of its KV head's tiles leaves a share of the result
@@ -166,7 +168,7 @@ constexpr int kSegment = 6;
 // B * max_seq_len * Hkv).
 struct Line {
   int tiles;             // of this lane's sequence, at least 1; 0: it has no rows on the plane
-  int incl, before;      // tiles of all heads up to it, and before the chunk
+  int incl, before;      // places of all heads up to it, and before the chunk
   unsigned active;       // lanes with rows
   int heads;             // KV heads before the chunk
   int chunk;
@@ -183,13 +185,15 @@ struct Line {
       if (s.T * (a.Hq / a.Hkv) > first_row) tiles = max(1, (s.len + kPage - 1) / kPage);
     }
     active = __ballot_sync(kFull, tiles > 0);
-    incl = tiles * a.Hkv;
+    incl = places(a);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += x;
     }
   }
+  // of this lane's sequence: kSegment more than tiles for each KV head
+  __device__ __forceinline__ int places(const TreeLaunch& a) const { return tiles ? (tiles + kSegment) * a.Hkv : 0; }
   __device__ __forceinline__ void next(const TreeLaunch& a, int first_row) {
     load(a, first_row, chunk + 32, before + total(), heads + __popc(active) * a.Hkv);
   }
@@ -202,7 +206,7 @@ struct Line {
 
 struct Division {
   int shares;            // by heads: CTAs of a head; 0: equal pieces
-  int used, each, more;  // equal pieces: CTAs, the first `more` with one tile more than `each`
+  int used, each, more;  // equal pieces: CTAs, the first `more` with one place more than `each`
 
   // Warp-collective; leaves the line at its first chunk.
   __device__ __forceinline__ Division(const TreeLaunch& a, int first_row, Line& line) {
@@ -227,16 +231,16 @@ struct Division {
     more = W - each * used;
     if (heads <= a.ctas) {
       const int n = min(a.ctas / heads, (most - 1) / a.min_tiles + 1);
-      if ((most - 1) / n + 1 <= each + kSegment) {
+      if ((most - 1) / n + 1 <= each) {
         shares = n;
         used = heads * n;
       }
     }
   }
   __device__ __forceinline__ int first(int cta) const { return each * cta + min(cta, more); }
-  __device__ __forceinline__ int cta_of(int tile) const {
+  __device__ __forceinline__ int cta_of(int place) const {
     const int split = (each + 1) * more;
-    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
+    return place < split ? place / (each + 1) : more + (place - split) / each;
   }
 };
 
@@ -270,22 +274,30 @@ struct Segments {
     }
   }
   __device__ __forceinline__ bool next(const TreeLaunch& a, int per, Segment& g) {
-    if (pos >= end) return false;
     const int row0 = blockIdx.y * per;
-    int l, first;  // the lane of the sequence; its first KV head, or tile of the line
-    if (shares) {
-      while (pos >= line.heads + __popc(line.active) * a.Hkv) line.next(a, row0);
-      const int lane = threadIdx.x & 31, mine = line.heads_at(a, lane);
-      l = __ffs(__ballot_sync(kFull, ((line.active >> lane) & 1) && pos >= mine && pos < mine + a.Hkv)) - 1;
-      first = line.heads_at(a, l);
-    } else {
+    int l, first, span;  // the lane of the sequence; its first KV head, or place of the line; places of tiles
+    for (;;) {
+      if (pos >= end) return false;
+      if (shares) {
+        while (pos >= line.heads + __popc(line.active) * a.Hkv) line.next(a, row0);
+        const int lane = threadIdx.x & 31, mine = line.heads_at(a, lane);
+        l = __ffs(__ballot_sync(kFull, ((line.active >> lane) & 1) && pos >= mine && pos < mine + a.Hkv)) - 1;
+        first = line.heads_at(a, l);
+        span = __shfl_sync(kFull, line.tiles, l);
+        break;
+      }
       while (pos >= line.before + line.total()) line.next(a, row0);
       l = __ffs(__ballot_sync(kFull, pos < line.before + line.incl)) - 1;
-      first = line.before + __shfl_sync(kFull, line.incl - line.tiles * a.Hkv, l);
+      first = line.before + __shfl_sync(kFull, line.incl - line.places(a), l);
+      span = __shfl_sync(kFull, line.tiles, l);
+      g.kv = (pos - first) / (span + kSegment);
+      first += g.kv * (span + kSegment);
+      if (pos - first < span) break;
+      pos = first + span + kSegment;  // behind a head's last tile
     }
     g.b = line.chunk + l;
     g.s = seq_of(a, g.b);
-    const int tiles = (g.s.len + kPage - 1) / kPage, span = max(1, tiles);
+    const int tiles = (g.s.len + kPage - 1) / kPage;
     g.row0 = row0;
     g.rows = min(per, g.s.T * (a.Hq / a.Hkv) - row0);
     if (shares) {
@@ -301,13 +313,12 @@ struct Segments {
       g.place = 0;
       return true;
     }
-    g.kv = (pos - first) / span;
-    g.t0 = pos - first - g.kv * span;
+    g.t0 = pos - first;
     const int n = min(span - g.t0, end - pos);
     g.nt = min(n, tiles - g.t0);
     g.whole = n == span;
-    g.place = pos == begin ? 0 : 1;
-    pos += n;
+    g.place = first <= begin ? 0 : 1;
+    pos += g.t0 + n == span ? n + kSegment : n;
     return true;
   }
 };

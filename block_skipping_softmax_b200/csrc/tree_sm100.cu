@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   while (b >= line.chunk + 32) line.next(a, plane * per);
   const int span = max(1, (s.len + kPage - 1) / kPage);
   const int head_at = line.heads_at(a, b - line.chunk) + kv;
-  const int first = line.before + __shfl_sync(kFull, line.incl - line.tiles * a.Hkv, b - line.chunk) + kv * span;
+  const int first = line.before + __shfl_sync(kFull, line.incl - line.places(a), b - line.chunk) +
+                    kv * (span + kSegment);
   const int rows = min(s.T * group, row0 + R);
   // Every CTA waits here, those without work too: what follows in the stream may
   // count on this kernel's end alone.
@@ -251,7 +252,7 @@ int check_sizes(int B, int max_q, int total_q, int Hq, int Hkv, int L, int d) {
     return ATTN_ERR_INVALID_ARG;
   if (Hq % Hkv != 0 || (d != 64 && d != 128)) return ATTN_ERR_INVALID_ARG;
   if (B > 65535 || Hq > 65535 || L > 0x7fffffff - kPage) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>((L + kPage - 1) / kPage) * B * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>((L + kPage - 1) / kPage + kSegment) * B * Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 

@@ -412,7 +412,7 @@ ATTN_API int attn_cache_read_e4m3(const void* K_codes, const void* V_codes, cons
  *   Errors: ATTN_ERR_INVALID_ARG as attn_decode_paged, for max_q outside 1..64,
  *   and for a workspace that is missing, unaligned or too small;
  *   ATTN_ERR_UNSUPPORTED for B or Hq from 65536, (num_pages + 1) * Hkv or
- *   ceil(max_seq_len / 64) * B * Hkv from 2^31, and off sm_100; ATTN_ERR_CUDA.
+ *   (ceil(max_seq_len / 64) + 6) * B * Hkv from 2^31, and off sm_100; ATTN_ERR_CUDA.
  */
 ATTN_API int attn_tree_paged(const void* q, const void* K_pages, const void* V_pages,
                              const int32_t* block_table, const int32_t* seq_lens,
