@@ -150,10 +150,10 @@ __device__ __forceinline__ Seq seq_of(const TreeLaunch& a, int b) {
 // A segment has its own start and end (queries, first copies, adding up the
 // warps' sums), worth about kSegment tiles: every KV head has as many places on
 // the line more than tiles, behind them, so that a piece across a head's end has
-// fewer tiles.  (By tiles alone the CTAs with two segments ended 4 to 12 us behind the
-// others.)  Heads are kept whole where their longest share is no longer than an
-// equal piece.  (One token over 8192 keys takes 13.5 us so, 18 with 0 or
-// with 64 in its place; 37 sequences over 4096 keys 62, 62 and 59.)
+// fewer tiles.  (By tiles alone the CTAs with two segments ended 3 to 12 us behind the
+// others: 16 ragged bf16 drafts of 8 tokens 280 us instead of 259, 64 tokens x 64
+// heads over 4 x 16384 keys 197 instead of 189.)  Heads are kept whole where their
+// longest share is no longer than an equal piece.
 //
 // A segment that is not all of its KV head's tiles leaves a share of the result
 // in one of the CTA's two places (only its first and its last segment can be
@@ -164,8 +164,7 @@ __device__ __forceinline__ Seq seq_of(const TreeLaunch& a, int b) {
 // same pages do so at about the same time, from L2.
 constexpr int kSegment = 6;
 
-// 32 sequences of the line; a plane has fewer than 2^31 tiles (the host checks
-// B * max_seq_len * Hkv).
+// 32 sequences of the line; a plane has fewer than 2^31 places (the host checks).
 struct Line {
   int tiles;             // of this lane's sequence, at least 1; 0: it has no rows on the plane
   int incl, before;      // places of all heads up to it, and before the chunk

@@ -18,10 +18,10 @@
 // e4m3 codes become fp16 in registers (or, for values of unusual scales, bf16),
 // so they cross shared memory once, as bytes.
 //
-// Measured, 16 sequences x 16384 keys, 8 KV heads: e4m3 of 128 with 4 rows 100 us
-// (5.4 TB/s of the 6.55 of a copy), with 16 rows 165 (issue-bound: a code costs as
-// much for 8 rows as for 16); of 64 with 4 rows 63; bf16 of 128 166 (6.5 TB/s), of
-// 64 92.  16 x 32768 e4m3 keys, 4 rows: 188-195 (5.7 TB/s); 250 with the rows on the
+// Measured, 16 sequences x 16384 keys, 8 KV heads: e4m3 of 128 with 4 rows 98 us
+// (5.6 TB/s of the 6.55 of a copy), with 16 rows 162 (issue-bound: a code costs as
+// much for 8 rows as for 16); of 64 with 4 rows 61; bf16 of 128 164 (6.5 TB/s), of
+// 64 90.  16 x 32768 e4m3 keys, 4 rows: 187 (5.9 TB/s); 250 with the rows on the
 // MMAs' long side and one warp that only copied.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -20,16 +20,18 @@
 // queries, and softmax warps without a row only keep step.
 //
 // Measured, 16 sequences x 16384 keys, 8 KV heads, with 16 / 64 / 128 rows a head:
-//   bf16 of 128  168 / 184 / 206 us   of 64  102 / 124 / 148
-//   e4m3 of 128  186 / 207 / 239      of 64  139 (32 rows) / 168 / 200
-// bf16 is bound by HBM up to 64 rows (6.3 TB/s).  With 512 rows a head (64 tokens x
-// 64 heads over 4 x 16384 keys: 195 us with the merge, 704 TFLOP/s) the tensor pipe, the ex2 unit
-// and the issue slots are each busy for 46 to 49% of the time: what counts is the
-// latency of S, softmax and P, with two warps a scheduler to hide it.  e4m3 adds
-// the latency of the conversion, and more warps to the same schedulers.  Slower:
-// codes of K straight into 8-bit MMAs, the query as two e4m3 terms (230 us instead
-// of 210 with 64 rows); two softmax warps to a row, half the keys each (bf16 219
-// instead of 206 with 128 rows, 145 instead of 123 for heads of 64 with 64).
+//   bf16 of 128  169 / 177 / 195 us   of 64  100 / 118 / 140
+//   e4m3 of 128  186 / 202 / 231      of 64  141 (32 rows) / 163 / 194
+// bf16 is bound by HBM up to 64 rows (6.1 TB/s and more).  With 512 rows a head (64
+// tokens x 64 heads over 4 x 16384 keys: 147 us and 12 of the merge, 189 a pass) the
+// tensor pipe, the ex2 unit and the issue slots are each busy for 46 to 49% of the
+// time: what counts is the latency of S, softmax and P, with two warps a scheduler
+// to hide it.  e4m3 adds the latency of the conversion, and more warps to the same
+// schedulers.  A segment's change costs 7 us: 3 for O, 3 for Q, 1 for the first S;
+// writing Q ahead of O gained nothing.  Slower: codes of K straight into 8-bit MMAs,
+// the query as two e4m3 terms (230 us against 210 then, with 64 rows); two softmax
+// warps to a row, half the keys each (bf16 219 against 206 with 128 rows, 145
+// against 123 for heads of 64 with 64).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -202,9 +202,9 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
   Plan p{};
   const long long rows = static_cast<long long>(max_q) * (Hq / Hkv);
   // Rows of a CTA.  16 sequences x 16384 keys, 8 KV heads of 128: e4m3 with 4 rows a
-  // head 100 us by 8s and 183 by 128s, with 16 rows 165 by 16s and 186 by 128s;
-  // bf16 166 and 165 with 4 rows (but one sequence of 500 keys 11.0 and 14.4), 186 and
-  // 168 with 16.
+  // head 98 us by 8s and 183 by 128s, with 16 rows 162 by 16s and 186 by 128s;
+  // bf16 164 and 165 with 4 rows (but one sequence of 500 keys 11 and 14.4), 186 and
+  // 165 with 16.
   p.per = rows <= 8 ? 8 : rows <= 16 && e4m3 ? 16 : kManyRows;
   p.planes = static_cast<int>((rows + p.per - 1) / p.per);
   const long long tiles = (L + kPage - 1) / kPage, heads = static_cast<long long>(B) * Hkv;
@@ -214,7 +214,7 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
   // heads are more than the CTAs that run at once and rounds of them cost less
   // than equal pieces: in tiles, rounds * (tiles + kSegment) against the equal piece
   // and its segments.  (16 x 512 e4m3 keys, 1 token: 10.2 us, 11.5 divided; 16 x 1024
-  // 14.4 and 15.0, but one sequence of 1024 14.1 and 11.1; 100 x 900 keys 47.2 and 48.9.)
+  // 14.4 and 15.2, but one sequence of 1024 14.1 and 10.5; 100 x 900 keys 47 and 49.)
   const long long rounds = (heads + fit - 1) / fit;
   if (tiles <= 8 || (rounds > 1 && 2 * rounds * (tiles + kSegment) <
                                        2 * (heads * tiles / fit) + (2 * heads / fit + 3) * kSegment)) {
@@ -222,8 +222,8 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
     p.ctas = static_cast<int>(heads);
     return p;
   }
-  // No CTA without four tiles: one token over 8192 keys 13.6 us, 17.1 from one or two
-  // tiles on, where the merge has more to add up (4 tokens over 1024 keys 11.1, 10.2
+  // No CTA without four tiles: one token over 8192 keys 13 us, 17 from one or two
+  // tiles on, where the merge has more to add up (4 tokens over 1024 keys 10.5, 10.2
   // from one tile on).
   p.min_tiles = 4;
   const long long most = (tiles * heads + p.min_tiles - 1) / p.min_tiles;
