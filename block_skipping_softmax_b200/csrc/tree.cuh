@@ -151,9 +151,10 @@ __device__ __forceinline__ Seq seq_of(const TreeLaunch& a, int b) {
 // warps' sums), worth about kSegment tiles: every KV head has as many places on
 // the line more than tiles, behind them, so that a piece across a head's end has
 // fewer tiles.  (By tiles alone the CTAs with two segments ended 3 to 12 us behind the
-// others: 16 ragged bf16 drafts of 8 tokens 280 us instead of 259, 64 tokens x 64
-// heads over 4 x 16384 keys 197 instead of 189.)  Heads are kept whole where their
-// longest share is no longer than an equal piece.
+// others: 64 tokens x 64 heads over 4 x 16384 keys 155 us before the merge instead of
+// 147; under a load of seconds, where the power limit holds the clocks down, a pass
+// 196 instead of 194.)  Heads are kept whole where their longest share is no longer
+// than an equal piece.
 //
 // A segment that is not all of its KV head's tiles leaves a share of the result
 // in one of the CTA's two places (only its first and its last segment can be

@@ -23,8 +23,8 @@
 //   bf16 of 128  169 / 177 / 195 us   of 64  100 / 118 / 140
 //   e4m3 of 128  186 / 202 / 231      of 64  141 (32 rows) / 163 / 194
 // bf16 is bound by HBM up to 64 rows (6.1 TB/s and more).  With 512 rows a head (64
-// tokens x 64 heads over 4 x 16384 keys: 147 us and 12 of the merge, 189 a pass) the
-// tensor pipe, the ex2 unit and the issue slots are each busy for 46 to 49% of the
+// tokens x 64 heads over 4 x 16384 keys: 147 us and 12 of the merge; 194 a pass under
+// a load of seconds, which the power limit slows) the tensor pipe, the ex2 unit and the issue slots are each busy for 46 to 49% of the
 // time: what counts is the latency of S, softmax and P, with two warps a scheduler
 // to hide it.  e4m3 adds the latency of the conversion, and more warps to the same
 // schedulers.  A segment's change costs 7 us: 3 for O, 3 for Q, 1 for the first S;
