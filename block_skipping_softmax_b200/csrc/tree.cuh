@@ -140,8 +140,11 @@ __device__ __forceinline__ Seq seq_of(const TreeLaunch& a, int b) {
   return s;
 }
 
-// The work of one plane (row block `plane` of every sequence that has one) is
-// the line of all its tiles: sequences, KV heads and tiles, in this order.  It
+// The host either gives every KV head of every sequence a CTA of its own, which
+// finds it without looking at other sequences (1000 sequences of 500 keys: 201 us,
+// 464 by way of the line), or has the device divide the work by the lengths:
+// the work of one plane (row block `plane` of every sequence that has one) is
+// the line of all its tiles, sequences, KV heads and tiles in this order.  It
 // is divided among the plane's CTAs in one of two ways.
 //   By heads: every KV head's tiles go to `shares` CTAs of their own.
 //   Equal pieces: the line is cut into pieces of the same cost, whatever the
@@ -173,17 +176,18 @@ struct Line {
   int heads;             // KV heads before the chunk
   int chunk;
 
+  // tiles of sequence b, 0 without rows on the plane
+  __device__ __forceinline__ static int tiles_of(const TreeLaunch& a, int b, int first_row) {
+    const Seq s = seq_of(a, b);
+    return s.T * (a.Hq / a.Hkv) > first_row ? max(1, (s.len + kPage - 1) / kPage) : 0;
+  }
   // Warp-collective: the sequences from `at` on.
   __device__ __forceinline__ void load(const TreeLaunch& a, int first_row, int at, int tiles_before, int heads_before) {
     const int lane = threadIdx.x & 31;
     chunk = at;
     before = tiles_before;
     heads = heads_before;
-    tiles = 0;
-    if (at + lane < a.B) {
-      const Seq s = seq_of(a, at + lane);
-      if (s.T * (a.Hq / a.Hkv) > first_row) tiles = max(1, (s.len + kPage - 1) / kPage);
-    }
+    tiles = at + lane < a.B ? tiles_of(a, at + lane, first_row) : 0;
     active = __ballot_sync(kFull, tiles > 0);
     incl = places(a);
 #pragma unroll
@@ -211,21 +215,18 @@ struct Division {
   // Warp-collective; leaves the line at its first chunk.
   __device__ __forceinline__ Division(const TreeLaunch& a, int first_row, Line& line) {
     line.load(a, first_row, 0, 0, 0);
-    int most = line.tiles;
-    while (line.chunk + 32 < a.B) {
-      line.next(a, first_row);
-      most = max(most, line.tiles);
+    int most = line.tiles, W = line.places(a), heads = line.tiles ? a.Hkv : 0;
+    for (int b = 32 + (threadIdx.x & 31); b < a.B; b += 32) {
+      const int tiles = line.tiles_of(a, b, first_row);
+      most = max(most, tiles);
+      W += tiles ? (tiles + kSegment) * a.Hkv : 0;
+      heads += tiles ? a.Hkv : 0;
     }
     most = __reduce_max_sync(kFull, most);
-    const int W = line.before + line.total(), heads = line.heads + __popc(line.active) * a.Hkv;
-    if (a.B > 32) line.load(a, first_row, 0, 0, 0);
+    W = __reduce_add_sync(kFull, W);
+    heads = __reduce_add_sync(kFull, heads);
     shares = used = each = more = 0;
     if (W == 0) return;
-    if (a.min_tiles == 0) {
-      shares = 1;
-      used = heads;
-      return;
-    }
     used = max(1, min(a.ctas, (W - 1) / a.min_tiles + 1));
     each = W / used;
     more = W - each * used;
@@ -259,8 +260,15 @@ struct Segments {
   int shares, begin, pos, end;  // by heads: begin is the share, pos the KV head, end one further
 
   __device__ __forceinline__ void start(const TreeLaunch& a, int per) {
-    const Division d(a, blockIdx.y * per, line);
     const int i = blockIdx.x;
+    if (a.min_tiles == 0) {  // a CTA for each KV head of each sequence
+      shares = 0;
+      begin = 0;
+      pos = i;
+      end = i + 1;
+      return;
+    }
+    const Division d(a, blockIdx.y * per, line);
     shares = d.shares;
     begin = pos = end = 0;
     if (i >= d.used) return;
@@ -275,6 +283,20 @@ struct Segments {
   }
   __device__ __forceinline__ bool next(const TreeLaunch& a, int per, Segment& g) {
     const int row0 = blockIdx.y * per;
+    if (a.min_tiles == 0) {
+      if (pos >= end) return false;
+      g.b = pos / a.Hkv;
+      g.kv = pos - g.b * a.Hkv;
+      ++pos;
+      g.s = seq_of(a, g.b);
+      g.row0 = row0;
+      g.rows = min(per, g.s.T * (a.Hq / a.Hkv) - row0);
+      g.t0 = 0;
+      g.nt = (g.s.len + kPage - 1) / kPage;
+      g.whole = true;
+      g.place = 0;
+      return g.rows > 0;
+    }
     int l, first, span;  // the lane of the sequence; its first KV head, or place of the line; places of tiles
     for (;;) {
       if (pos >= end) return false;

@@ -213,8 +213,8 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
   // A CTA for each KV head, and no merge, where its tiles are few, or where the
   // heads are more than the CTAs that run at once and rounds of them cost less
   // than equal pieces: in tiles, rounds * (tiles + kSegment) against the equal piece
-  // and its segments.  (16 x 512 e4m3 keys, 1 token: 10.2 us, 11.5 divided; 16 x 1024
-  // 14.4 and 15.2, but one sequence of 1024 14.1 and 10.5; 100 x 900 keys 47 and 49.)
+  // and its segments.  (16 x 512 e4m3 keys, 1 token: 9.4 us, 11.5 divided; 16 x 1024
+  // 13.6 and 15.2, but one sequence of 1024 13.3 and 10.5; 100 x 900 keys 43 and 49.)
   const long long rounds = (heads + fit - 1) / fit;
   if (tiles <= 8 || (rounds > 1 && 2 * rounds * (tiles + kSegment) <
                                        2 * (heads * tiles / fit) + (2 * heads / fit + 3) * kSegment)) {

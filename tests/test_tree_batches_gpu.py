@@ -58,6 +58,8 @@ def check(c, o):
     (200, 4, 1, 1, 900, 64),     # more heads than CTAs
     (90, 4, 4, 33, 700, 64),     # the same, in two planes of rows
     (300, 2, 2, 2, 400, 128),    # few tiles: a CTA a head
+    (600, 1, 2, 9, 100, 64),     # the same, of many rows
+    (130, 1, 2, 3, 3000, 64),    # pieces over several times 32 sequences
 ])
 def test_many_ragged_sequences(cache, B, Hkv, g, T, most, d):
     rng = random.Random(B)
