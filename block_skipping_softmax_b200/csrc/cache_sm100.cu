@@ -14,9 +14,10 @@
 // each vector; a group of lanes takes up to four vectors, all loaded before the
 // first is reduced.  What held it back beside HBM was the issue of instructions,
 // so the lanes share what a vector costs once (see Row), and maxima are taken
-// two to a word: 4 prompts of 4099 tokens x 8 heads of 128 are written in 19.3 us
-// (5.3 TB/s; 27.4 when every lane found its vectors and reduced in fp32), and
-// 2 x 32768 tokens read back in 71 us (5.7 TB/s; 88 before), of 6.55 TB/s for a copy.
+// two to a word: 4 prompts of 4099 tokens x 8 heads of 128 are written in 18.9 us
+// (5.4 TB/s; 19.6 by CTAs of 256 threads, 20.5 of 512; 27.4 when every lane found
+// its vectors and reduced in fp32), and 2 x 32768 tokens read back in 71 us (5.7
+// TB/s; 88 before), of 6.55 TB/s for a copy.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +31,7 @@ namespace bss {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPage = kDecodeTile;  // keys of a page
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -202,7 +203,7 @@ int launch_r(const CacheArgs& a, cudaStream_t s) {
 
 // Vectors of a group: one where the launch fits the 148 SMs at once, else four.
 // (65536 tokens read back: 120 us by ones, 71 by fours; 4 x 4099 written: 32 and
-// 19; 16 tokens of 8 heads of 128 written: 1.95 us by ones, 2.2 by fours.)
+// 19; 16 tokens of 8 heads of 128 written: 2.0 us by ones, 2.2 by fours.)
 template <int D, bool WRITE>
 int launch_d(const CacheArgs& a, cudaStream_t s) {
   constexpr int kGroups = kThreads / (D / 8);

@@ -19,8 +19,8 @@
 // tokens' sines and cosines are made once, into shared memory, while the first
 // rows are on their way.
 //
-// 8192 tokens x 40 heads of 128: 29.7 us, 5.7 TB/s of the 6.55 of a copy; 30011
-// x 20 heads of 64: 29.9 us, 5.1 TB/s, with a third of the issue slots idle and
+// 8192 tokens x 40 heads of 128: 28.8 us, 5.8 TB/s of the 6.55 of a copy; 30011
+// x 20 heads of 64: 29.2 us, 5.3 TB/s, with a third of the issue slots idle and
 // about 40 KB in flight an SM.  Two values to an fp32 instruction changed nothing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,7 +35,7 @@ namespace bss {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // 256: 2% slower, by the tails of the launch
 constexpr unsigned kFull = 0xffffffffu;
 
 struct RopeArgs {
@@ -63,7 +63,7 @@ __device__ __forceinline__ void unpack8(const uint4 u, float (&f)[8]) {
 
 // CTA (x, y): kGroups / groups tokens, their heads [y * heads, ...).
 template <int D, bool NORM>
-__global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 10) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kLanes = D / 16;              // lanes of a row
   constexpr int kGroups = kThreads / kLanes;  // rows at a time
   extern __shared__ __align__(16) float s_angle[];  // [token][cos, sin][rot / 2]
@@ -188,8 +188,8 @@ void launch_d(RopeArgs& a, cudaStream_t s) {
     a.heads = kGroups;
   } else {
     // the most groups a token that leave at most a tenth of them idle (with one
-    // token a CTA, 8192 x 40 heads take 39.9 us instead of 29.7, 30011 x 20 heads
-    // of 64 110 instead of 29.9)
+    // token to a CTA of 256 threads, 8192 x 40 heads took 39.9 us instead of 29.7,
+    // 30011 x 20 heads of 64 110 instead of 29.9)
     auto idle = [&](int g) { return 10 * (((a.H + g - 1) / g) * g - a.H) > ((a.H + g - 1) / g) * g; };
     while (a.groups > 1 && idle(a.groups)) a.groups /= 2;
   }
