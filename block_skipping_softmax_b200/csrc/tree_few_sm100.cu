@@ -421,13 +421,21 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float2 x = log2_p<E4M3>(make_float2(sc[b][t][2 * h], sc[b][t][2 * h + 1]), from, by);
-            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            float p0 = ex2(x.x), p1 = ex2(x.y);
             uint32_t w;
             if (f16) {
               w = pack_f16x2(p0, p1);
               sum[t][0] += p0;
               sum[t][1] += p1;
             } else {
+              if constexpr (E4M3) {
+                // a value whose scale is NaN reaches every row that sees the key, at any p
+                const float v = lds_f32(scales + C::kScaleBytes + 4 * (16 * b + 8 * h + key_n));
+                if (v != v) {
+                  if (sc[b][t][2 * h] != neg_inf()) p0 = v;
+                  if (sc[b][t][2 * h + 1] != neg_inf()) p1 = v;
+                }
+              }
               w = pack_bf16x2(p0, p1);
               sum[t][0] += __uint_as_float(w << 16);
               sum[t][1] += __uint_as_float(w & 0xffff0000u);
@@ -482,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                 mma_16816<true>(o[j][t], a0, a1, a2, a3, pb[b][t][0], pb[b][t][1]);
             }
           } else {
-            // The value scale goes to P, whose bf16 holds its exponent.  An
-            // unseen key's scale may be NaN: 0 stays 0.
+            // The value scale goes to P, whose bf16 holds its exponent.  The
+            // scale of a key that the row does not see may be NaN: 0 stays 0.
             uint32_t pv[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
