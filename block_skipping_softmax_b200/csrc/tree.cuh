@@ -106,7 +106,11 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 // instructions a code.  Probabilities carry 2^7, so that fp16 (up to 65504)
 // holds them from p = 2^8 down to 2^-31 of the reference maximum.
 constexpr int kPShift = 7;
-__device__ __forceinline__ bool fits_f16(float scale) { return scale >= pow2(-15) && scale <= pow2(7); }
+// How far a scale lies above 2^-15, in steps of floats: kFitsF16 and less up to
+// 2^7, more for larger, smaller, negative ones and NaN.  The maximum of several
+// says whether all fit.
+__device__ __forceinline__ uint32_t over_f16(float scale) { return __float_as_uint(scale) - 0x38000000u; }
+constexpr uint32_t kFitsF16 = 0x43000000u - 0x38000000u;
 
 // The exponents of two probabilities: (score - reference) * scale, in log2 units.
 // minus(reference) is 0 where nothing has been seen so far: then all p are 0.

@@ -388,19 +388,30 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           }
         }
       }
-      // ---- e4m3: V as fp16 where this warp's value scales allow (see fits_f16)
+      // ---- e4m3: V as fp16 where this warp's value scales allow (see over_f16)
       float vs[KB][4];  // scales of the keys of this lane's V rows: key_lo, + kStep, + 8 of each
       bool f16 = false;
       if constexpr (E4M3) {
-        f16 = true;
+        uint32_t over = 0;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             vs[b][e] = lds_f32(scales + C::kScaleBytes + 4 * (16 * b + 8 * (e >> 1) + key_lo + (e & 1) * LN::kStep));
-            f16 = f16 && fits_f16(vs[b][e]);
+            over = max(over, over_f16(vs[b][e]));
           }
-        f16 = __all_sync(kFull, f16 || bad_page);
+        f16 = __all_sync(kFull, over <= kFitsF16 || bad_page);
+        if (!f16 && tail) {  // what lies behind the last key does not decide
+          over = 0;
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (key0 + 16 * b + 8 * (e >> 1) + key_lo + (e & 1) * LN::kStep >= sg.s.len) vs[b][e] = 1.f;
+              over = max(over, over_f16(vs[b][e]));
+            }
+          f16 = __all_sync(kFull, over <= kFitsF16);
+        }
         if (bad_page) {
 #pragma unroll
           for (int b = 0; b < KB; ++b)

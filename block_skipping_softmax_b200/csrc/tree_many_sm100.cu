@@ -653,15 +653,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           const uint32_t scales = sbase + C::kOffScale + s * C::kScaleBytes;  // K, V
           const uint32_t dst = sbase + C::kOffConv + (is_v * C::kOperands + n % C::kOperands) * C::kTile;
           const bool zero = misc->bad_page[s] != 0;
-          bool fits = true;
+          const int key0 = (sg.t0 + j) * kPage;
+          // the scales of this sequence's keys decide, not what lies behind the last one
+          uint32_t over = 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) fits = fits && fits_f16(lds_f32(scales + (32 * x + lane) * 4));
-          const bool plain = __all_sync(kFull, fits || zero);
+          for (int x = 0; x < 4; ++x) {  // K's, then V's
+            const uint32_t o = over_f16(lds_f32(scales + (32 * x + lane) * 4));
+            if (key0 + 32 * (x & 1) + lane < sg.s.len) over = max(over, o);
+          }
+          const bool plain = __all_sync(kFull, over <= kFitsF16 || zero);
           // A thread takes 16-code chunks, eight neighbours the same chunk of
           // eight keys: with both tiles swizzled no read or write meets a bank twice.
           constexpr int kChunks = D / 16, kM = kPage * kChunks / kN;
           const bool check = is_v && j >= first_tail;
-          const int key0 = (sg.t0 + j) * kPage;
           uint32_t bad0 = 0, bad1 = 0;  // keys 0-31 and 32-63
           auto place = [&](int m, int& key, int& c) {
             const int x = m * kN + t;
@@ -690,7 +694,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
               uint4 u = load(key, c);
               float sc = plain ? lds_f32(scales + (is_v * kPage + key) * 4) : 1.f;
               if (zero) sc = 0.f;
-              if (check && key0 + key >= sg.s.len) u = make_uint4(0, 0, 0, 0);
+              if (check && key0 + key >= sg.s.len) {
+                u = make_uint4(0, 0, 0, 0);
+                sc = 0.f;  // it may be NaN
+              }
               const uint32_t s2 = pack_f16x2(sc, sc), x[4] = {u.x, u.y, u.z, u.w};
               uint32_t o[8];
 #pragma unroll
