@@ -365,6 +365,13 @@ __device__ __forceinline__ uint64_t bits_of(const TreeLaunch& a, const Seq& s, i
   return a.mask ? a.mask[s.tok0 + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
 }
 
+// What a row without a sum gets, with these bits: 0 if it sees no key, else NaN:
+// its scores are all -inf, over which softmax has no value.
+__device__ __forceinline__ float without_sum(const Seq& s, uint64_t bits) {
+  const bool sees = s.prefix > 0 || (bits & (s.len >= 64 ? ~0ull : (1ull << s.len) - 1)) != 0;
+  return sees ? __int_as_float(0x7fffffff) : 0.f;
+}
+
 // Tensor map over a pool of e4m3 codes [groups, 64, D], d fastest: boxes of
 // `keys` keys, rows swizzled as 128 bytes (D = 128) or 64 (D = 64); groups past
 // the end read as zeros.

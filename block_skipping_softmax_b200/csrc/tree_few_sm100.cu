@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           const int r = 8 * t + 2 * q + c;
           if (r >= sg.rows) continue;
           const bool empty = den[t][c] == 0.f;  // a row that sees nothing here
-          const float inv = empty ? 0.f : 1.f / den[t][c];
+          const float none = without_sum(sg.s, bits[t][c]), inv = empty ? 0.f : 1.f / den[t][c];
           const size_t share = share_at(a, kRows, blockIdx.y, blockIdx.x, sg.place, r);
           const size_t at = row_at(a, sg, r);
           if (!sg.whole && n == 0)
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int j = 4 * x + (e >> 1), k = 2 * (e & 1) + c;
-              f[e] = empty ? 0.f : (o[j][t][k] + red[((j * NT + t) * 4 + k) * 32 + lane]) * inv;
+              f[e] = empty ? none : (o[j][t][k] + red[((j * NT + t) * 4 + k) * 32 + lane]) * inv;
             }
             if (sg.whole) {
               *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + d0) =

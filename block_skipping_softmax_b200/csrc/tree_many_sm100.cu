@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
       if (active) {
         tc_fence_after();
         const bool empty = l_sum == 0.f;  // a row that sees nothing here
-        const float inv = empty ? 0.f : 1.f / l_sum;
+        const float none = without_sum(sg.s, bits), inv = empty ? 0.f : 1.f / l_sum;
         const size_t share = share_at(a, kRows, blockIdx.y, blockIdx.x, sg.place, r);
         if (valid && !sg.whole) a.lse[share] = empty ? neg_inf() : m_ref * mul + __log2f(l_sum) - (E4M3 ? kPShift : 0);
         float* part = a.part + share * D;
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
           if (!valid) continue;
           float f[16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) f[c] = empty ? 0.f : __uint_as_float(o[c]) * inv;
+          for (int c = 0; c < 16; ++c) f[c] = empty ? none : __uint_as_float(o[c]) * inv;
           if (sg.whole) {
 #pragma unroll
             for (int c = 0; c < 16; c += 8)

@@ -5,9 +5,10 @@
 // T_b of its len_b cached ones.  Token i sees the whole prefix and drafted key
 // j iff bit j of its mask is set (its ancestors in the tree and itself), so
 //   o_i = sum_k p_ik v_k / sum_k p_ik,  p_ik = exp(q_i k_k / sqrt(d) - m_i)
-// over the keys that it sees; a token that sees none gets 0.  T_b = 1 is the
-// decode of single tokens.  With e4m3 codes key k is its codes times ks_k,
-// which scales a column of scores, and value k its codes times vs_k.
+// over the keys that it sees; a token that sees none gets 0 (one whose scores are
+// all -inf NaN).  T_b = 1 is the decode of single tokens.  With e4m3 codes key k is
+// its codes times ks_k, which scales a column of scores, and value k its codes
+// times vs_k.
 //
 // The rows that share a KV head are the T_b * g pairs of a token and a query
 // head of the group (row r: token r / g, head r % g).
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   };
   constexpr int kC = D / 32;
   auto write = [&](int row, const float (&num)[kC], float den) {
-    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const float inv = den == 0.f ? without_sum(s, bits_of(a, s, row / group)) : 1.f / den;  // num is 0 then
     const size_t at = static_cast<size_t>(s.tok0 + row / group) * a.Hq + kv * group + row % group;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + at * D + lane * kC;
 #pragma unroll

@@ -401,9 +401,12 @@ ATTN_API int attn_cache_read_e4m3(const void* K_codes, const void* V_codes, cons
  *              Null: a chain, token i sees drafted keys 0 to i; with one token
  *              a sequence this is the decode of single tokens.
  *   max_q      1 to 64.
- *   A token that sees no key gets 0.  Slots past len_b may hold anything.  A
- *   drafted key or value that is not finite reaches only the tokens that see
- *   it, which then holds NaN.
+ *   A token that sees no key gets 0.  Slots past len_b may hold anything, which
+ *   changes no bit of o.  What is not finite goes by the formula: a query with
+ *   inf or NaN gives NaN (of scores that are all -inf too), a key reaches the
+ *   tokens that see it by its score (of -inf: no weight), a value by its product
+ *   with their weight, or, drafted, as NaN in all elements or in its own.  None
+ *   reaches a token that does not see it.
  *   ws         device workspace of attn_tree_workspace_bytes(...) bytes, 256-byte
  *              aligned; null where that is 0.  Its contents do not matter, and
  *              are not used by a later call.  Calls that may overlap on the GPU
