@@ -100,7 +100,7 @@ struct TreeLaunch {
   int ctas;       // CTAs of a plane: grid.x
   int min_tiles;  // least work of a CTA; 0: no KV head's tiles are divided
   float* part;    // [planes, ctas, 2, rows of a CTA, d] fp32: shares of a KV head's keys
-  float* lse;     // [planes, ctas, 2, rows of a CTA]
+  float2* sums;   // [planes, ctas, 2, rows of a CTA]: reference score in log2 units, sum of 2^(score - reference)
   int* status;
   unsigned long long wait_limit_ns;
   cudaStream_t stream;

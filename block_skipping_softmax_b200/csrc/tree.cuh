@@ -356,7 +356,7 @@ __device__ __forceinline__ size_t row_at(const TreeLaunch& a, const Segment& g, 
   if (token) *token = t;
   return static_cast<size_t>(g.s.tok0 + t) * a.Hq + g.kv * group + (g.row0 + r) - t * group;
 }
-// its row of part and lse
+// its row of part and sums
 __device__ __forceinline__ size_t share_at(const TreeLaunch& a, int per, int plane, int cta, int place, int r) {
   return ((static_cast<size_t>(plane) * a.ctas + cta) * 2 + place) * per + r;
 }

@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           const size_t share = share_at(a, kRows, blockIdx.y, blockIdx.x, sg.place, r);
           const size_t at = row_at(a, sg, r);
           if (!sg.whole && n == 0)
-            a.lse[share] = empty ? neg_inf() : M[t][c] * mul[t][c] + __log2f(den[t][c]) - (E4M3 ? kPShift : 0);
+            a.sums[share] = make_float2(M[t][c] * mul[t][c], den[t][c] * (E4M3 ? pow2(-kPShift) : 1.f));
           // this lane's columns, in runs of 8: block pair j holds columns
           // 2j and 2j + 1 of the lane's chunk of 16 codes, or of 8 values a panel
 #pragma unroll

@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 2)
         const bool empty = l_sum == 0.f;  // a row that sees nothing here
         const float none = without_sum(sg.s, bits), inv = empty ? 0.f : 1.f / l_sum;
         const size_t share = share_at(a, kRows, blockIdx.y, blockIdx.x, sg.place, r);
-        if (valid && !sg.whole) a.lse[share] = empty ? neg_inf() : m_ref * mul + __log2f(l_sum) - (E4M3 ? kPShift : 0);
+        if (valid && !sg.whole) a.sums[share] = make_float2(m_ref * mul, l_sum * (E4M3 ? pow2(-kPShift) : 1.f));
         float* part = a.part + share * D;
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + at * D;
 #pragma unroll 1

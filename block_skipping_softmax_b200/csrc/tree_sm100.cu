@@ -75,101 +75,100 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
     return div.shares > span && span * i / div.shares == span * (i + 1) / div.shares;
   };
   constexpr int kC = D / 32;
-  auto write = [&](int row, const float (&num)[kC], float den) {
-    const float inv = den == 0.f ? without_sum(s, bits_of(a, s, row / group)) : 1.f / den;  // num is 0 then
+  // The reference and the sum of a share go together: of shares with the same
+  // reference, however large, each counts by its sum.  A share's result is its
+  // mean already, so a weighted mean of them stays within their range.
+  auto weight = [](float2 l, float M) { return l.y == 0.f ? 0.f : l.x == M ? l.y : l.y * ex2(l.x - M); };
+  auto write = [&](int row, const float (&mean)[kC], float den) {
+    const float none = den == 0.f ? without_sum(s, bits_of(a, s, row / group)) : 0.f;
     const size_t at = static_cast<size_t>(s.tok0 + row / group) * a.Hq + kv * group + row % group;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + at * D + lane * kC;
 #pragma unroll
     for (int e = 0; e < kC; e += 2)
-      *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(num[e] * inv, num[e + 1] * inv);
+      *reinterpret_cast<uint32_t*>(out + e) = den == 0.f ? pack_bf16x2(none, none) : pack_bf16x2(mean[e], mean[e + 1]);
   };
   if (R > 1 && c1 - c0 < kFew) {  // all loads of two rows at once
 #pragma unroll 2
     for (int row = row0; row < rows; ++row) {
-      float l[kFew], M = neg_inf(), den = 0.f, num[kC];
-      float2 v[kFew][kC / 2];
+      float2 l[kFew], v[kFew][kC / 2];
+      float w[kFew], M = neg_inf(), den = 0.f, mean[kC];
 #pragma unroll
       for (int i = 0; i < kFew; ++i) {
         const int c = min(c0 + i, c1);
         const size_t at = share_at(a, per, plane, c, c == c0 ? place0 : 0, row - plane * per);
-        l[i] = c0 + i > c1 || empty(c) ? neg_inf() : a.lse[at];
+        l[i] = c0 + i > c1 || empty(c) ? make_float2(neg_inf(), 0.f) : a.sums[at];
 #pragma unroll
         for (int e = 0; e < kC / 2; ++e) v[i][e] = reinterpret_cast<const float2*>(a.part + at * D + lane * kC)[e];
       }
 #pragma unroll
-      for (int i = 0; i < kFew; ++i) M = fmaxf(M, l[i]);
+      for (int i = 0; i < kFew; ++i) M = fmaxf(M, l[i].x);
 #pragma unroll
-      for (int e = 0; e < kC; ++e) num[e] = 0.f;
+      for (int i = 0; i < kFew; ++i) den += w[i] = weight(l[i], M);
+      const float inv = 1.f / den;
+#pragma unroll
+      for (int e = 0; e < kC; ++e) mean[e] = 0.f;
 #pragma unroll
       for (int i = 0; i < kFew; ++i) {
-        // 0: nothing seen there, and its sums perhaps not written
-        const float w = l[i] == neg_inf() ? 0.f : l[i] == M ? 1.f : ex2(l[i] - M);
-        den += w;
-        if (w != 0.f) {
+        if (w[i] != 0.f) {  // else an empty share, perhaps: its result was not written
 #pragma unroll
           for (int e = 0; e < kC / 2; ++e) {
-            num[2 * e] = fmaf(w, v[i][e].x, num[2 * e]);
-            num[2 * e + 1] = fmaf(w, v[i][e].y, num[2 * e + 1]);
+            mean[2 * e] = fmaf(w[i] * inv, v[i][e].x, mean[2 * e]);
+            mean[2 * e + 1] = fmaf(w[i] * inv, v[i][e].y, mean[2 * e + 1]);
           }
         }
       }
-      write(row, num, den);
+      write(row, mean, den);
     }
     return;
   }
 #pragma unroll 1
   for (int row = row0; row < rows; ++row) {
     auto share = [&](int c) { return share_at(a, per, plane, c, c == c0 ? place0 : 0, row - plane * per); };
-    float M = neg_inf();
-    for (int c = c0 + lane; c <= c1; c += 32)
-      if (!empty(c)) M = fmaxf(M, a.lse[share(c)]);
+    auto sums = [&](int c) { return c > c1 || empty(c) ? make_float2(neg_inf(), 0.f) : a.sums[share(c)]; };
+    const float2 own = sums(c0 + lane);  // the others, if there are more than 32, are read again
+    float M = own.x;
+    for (int c = c0 + lane + 32; c <= c1; c += 32) M = fmaxf(M, sums(c).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float num[kC], den = 0.f;
+    const float w_own = weight(own, M);
+    float mean[kC], den = w_own;
+    for (int c = c0 + lane + 32; c <= c1; c += 32) den += weight(sums(c), M);
 #pragma unroll
-    for (int c = 0; c < kC; ++c) num[c] = 0.f;
-    for (int base = c0 + part; base <= c1; base += 32 * W) {
-      // lane i: weight of share base + i W
-      float w = 0.f;
-      if (base + lane * W <= c1 && !empty(base + lane * W)) {
-        const float l = a.lse[share(base + lane * W)];
-        w = l == neg_inf() ? 0.f : l == M ? 1.f : ex2(l - M);  // 0: nothing seen there
-      }
-      den += w;
-      const int n = min(32, (c1 - base) / W + 1);
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
+    const float inv = 1.f / den;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) mean[c] = 0.f;
+    for (int base = c0; base <= c1; base += 32) {
+      const float w = base == c0 ? w_own : weight(sums(base + lane), M);  // lane i: of share base + i
+      const int n = min(32, c1 - base + 1);
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float* x = a.part + share(base + i * W) * D + lane * kC;
+      for (int i = part; i < n; i += W) {
+        const float* x = a.part + share(base + i) * D + lane * kC;
         float2 v[kC / 2];
 #pragma unroll
         for (int e = 0; e < kC / 2; ++e) v[e] = reinterpret_cast<const float2*>(x)[e];
         const float wi = __shfl_sync(kFull, w, i);
-        if (wi != 0.f) {  // else an empty share, perhaps: its sums were not written
+        if (wi != 0.f) {
 #pragma unroll
           for (int e = 0; e < kC / 2; ++e) {
-            num[2 * e] = fmaf(wi, v[e].x, num[2 * e]);
-            num[2 * e + 1] = fmaf(wi, v[e].y, num[2 * e + 1]);
+            mean[2 * e] = fmaf(wi * inv, v[e].x, mean[2 * e]);
+            mean[2 * e + 1] = fmaf(wi * inv, v[e].y, mean[2 * e + 1]);
           }
         }
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
     if constexpr (W > 1) {
-      __shared__ float red[W][D + 1];
+      __shared__ float red[W][D];
 #pragma unroll
-      for (int e = 0; e < kC; ++e) red[part][lane * kC + e] = num[e];
-      if (lane == 0) red[part][D] = den;
+      for (int e = 0; e < kC; ++e) red[part][lane * kC + e] = mean[e];
       __syncthreads();
       if (part != 0) return;
 #pragma unroll
-      for (int x = 1; x < W; ++x) {
-        den += red[x][D];
+      for (int x = 1; x < W; ++x)
 #pragma unroll
-        for (int e = 0; e < kC; ++e) num[e] += red[x][lane * kC + e];
-      }
+        for (int e = 0; e < kC; ++e) mean[e] += red[x][lane * kC + e];
     }
-    write(row, num, den);
+    write(row, mean, den);
   }
 }
 
@@ -233,7 +232,7 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
   if (p.shares) {
     const size_t n = static_cast<size_t>(p.planes) * p.ctas * 2 * p.per;
     p.part_bytes = align256(n * d * sizeof(float));
-    p.bytes = p.part_bytes + align256(n * sizeof(float));
+    p.bytes = p.part_bytes + align256(n * sizeof(float2));
   }
   return p;
 }
@@ -274,7 +273,7 @@ int run_tree(TreeLaunch& a, void* ws, size_t ws_bytes, void* stream) {
   if (p.shares) {
     if (!ws || !ptr_aligned(ws, 256) || ws_bytes < p.bytes) return ATTN_ERR_INVALID_ARG;
     a.part = static_cast<float*>(ws);
-    a.lse = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_bytes);
+    a.sums = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.part_bytes);
   }
   int dev = 0;
   if ((st = device_context(&dev, &a.status)) != ATTN_OK) return st;
