@@ -407,6 +407,9 @@ ATTN_API int attn_cache_read_e4m3(const void* K_codes, const void* V_codes, cons
  *   tokens that see it by its score (of -inf: no weight), a value by its product
  *   with their weight, or, drafted, as NaN in all elements or in its own.  None
  *   reaches a token that does not see it.
+ *   Sums are held in fp32, their terms being a value times at most 2^8: results
+ *   are finite and exact to that if len_b max|v| stays below 2^120, and scores if
+ *   q k does.
  *   ws         device workspace of attn_tree_workspace_bytes(...) bytes, 256-byte
  *              aligned; null where that is 0.  Its contents do not matter, and
  *              are not used by a later call.  Calls that may overlap on the GPU
@@ -428,8 +431,11 @@ ATTN_API int attn_tree_paged(const void* q, const void* K_pages, const void* V_p
  * attn_tree_paged over a cache of e4m3 codes as attn_cache_write_e4m3 writes
  * it: key k of a page means K_codes * K_scales, value k V_codes * V_scales
  * (powers of two; 16-byte aligned).  Exact attention over the values that
- * attn_cache_read_e4m3 reads back; a key or value whose scale is NaN makes the
- * tokens that see it NaN.
+ * attn_cache_read_e4m3 reads back, with these limits: len_b max|v| below 2^113
+ * (terms of the sums carry up to 2^15) and max|k| up to 2^104 (scores are held at
+ * 2^14 to 2^15 of the query's largest element); an element of q smaller than 2^-28
+ * of the query's largest is off by up to 2^-40 of that one.  A key or value whose
+ * scale is NaN makes the tokens that see it NaN.
  */
 ATTN_API int attn_tree_paged_e4m3(const void* q, const void* K_codes, const void* V_codes,
                                   const float* K_scales, const float* V_scales,
