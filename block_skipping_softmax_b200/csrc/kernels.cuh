@@ -108,7 +108,7 @@ struct TreeLaunch {
 
 // rows of a CTA: 8, or 16 over e4m3 (tree_few_sm100.cu), with so many CTAs an SM
 int launch_tree_few(const TreeLaunch& a, int rows);
-int tree_few_ctas();
+int tree_few_ctas(int d, bool e4m3, int rows);
 int launch_tree_many(const TreeLaunch& a);  // 128 rows, 2 CTAs an SM (tree_many_sm100.cu)
 
 // Current device (sm_100 checked) and its device status word (api.cu).

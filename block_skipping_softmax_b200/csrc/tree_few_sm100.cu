@@ -19,10 +19,12 @@
 // so they cross shared memory once, as bytes.
 //
 // Measured, 16 sequences x 16384 keys, 8 KV heads: e4m3 of 128 with 4 rows 98 us
-// (5.6 TB/s of the 6.55 of a copy), with 16 rows 162 (issue-bound: a code costs as
-// much for 8 rows as for 16); of 64 with 4 rows 61; bf16 of 128 164 (6.5 TB/s), of
-// 64 90.  16 x 32768 e4m3 keys, 4 rows: 187 (5.9 TB/s); 250 with the rows on the
-// MMAs' long side and one warp that only copied.
+// (5.6 TB/s of the 6.55 of a copy), with 16 rows 112 (4.9 TB/s); of 64 with 4 rows
+// 58 and with 16 rows 75 (4.7 and 3.7 TB/s); bf16 of 128 166 (6.5 TB/s), of 64 90.
+// 16 x 32768 e4m3 keys, 4 rows: 187 (5.9 TB/s); 250 with the rows on the MMAs' long
+// side and one warp that only copied.  Heads of 128 with 16 rows take 231 registers
+// and 77 KB, two CTAs an SM; with three asked for, of which two fitted, the third
+// of the equal pieces came after the others, and 212 bytes were spilled (163 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,7 +41,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtas = 3;  // of an SM
+constexpr int kSmSmem = 233472;  // shared memory of an SM, of which every CTA takes 1 KB besides its own
 
 template <int D, bool E4M3, int NT>
 struct Cfg {
@@ -60,6 +62,9 @@ struct Cfg {
   static constexpr int kOffBar = kOffMax + 2 * kWarps * kRows * 4;  // [warp][stage]
   static constexpr int kOffMisc = kOffBar + kWarps * kStages * 8;   // abort
   static constexpr int kSmem = kOffMisc + 16 + 1024;
+  // CTAs of an SM, which the division of the work counts on
+  static constexpr int kCtas = E4M3 && D == 128 && NT == 2 ? 2 : 3;
+  static_assert(kCtas * (kSmem + 1024) <= kSmSmem, "all of them resident");
 };
 
 template <bool F16>
@@ -100,7 +105,7 @@ struct Lanes {
 };
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads, kCtas)
+__global__ void __launch_bounds__(kThreads, Cfg<D, E4M3, NT>::kCtas)
     tree_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ TreeLaunch a) {
   using C = Cfg<D, E4M3, NT>;
@@ -678,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 }
 
 template <int D, bool E4M3, int NT>
-int launch_t(const TreeLaunch& a) {
+int launch_t(const TreeLaunch& a, Cfg<D, E4M3, NT>) {
   using C = Cfg<D, E4M3, NT>;
   auto kern = tree_few_kernel<D, E4M3, NT>;
   static uint64_t attr_done = 0;  // one bit per device ordinal
@@ -698,23 +703,23 @@ int launch_t(const TreeLaunch& a) {
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-template <int D, bool E4M3>
-int launch_n(const TreeLaunch& a, int rows) {
-  switch (rows) {
-    case 8: return launch_t<D, E4M3, 1>(a);
-    case 16:
-      if constexpr (E4M3) return launch_t<D, E4M3, 2>(a);
-  }
+// f of the configuration for d, the cache and the rows of a CTA
+template <class F>
+int with_cfg(int d, bool e4m3, int rows, F f) {
+  if (!e4m3 && rows == 8) return d == 64 ? f(Cfg<64, false, 1>{}) : f(Cfg<128, false, 1>{});
+  if (e4m3 && rows == 8) return d == 64 ? f(Cfg<64, true, 1>{}) : f(Cfg<128, true, 1>{});
+  if (e4m3 && rows == 16) return d == 64 ? f(Cfg<64, true, 2>{}) : f(Cfg<128, true, 2>{});
   return ATTN_ERR_INVALID_ARG;
 }
 
 }  // namespace
 
-int tree_few_ctas() { return kCtas; }
+int tree_few_ctas(int d, bool e4m3, int rows) {
+  return with_cfg(d, e4m3, rows, [](auto c) { return decltype(c)::kCtas; });
+}
 
 int launch_tree_few(const TreeLaunch& a, int rows) {
-  if (a.d == 64) return a.k_scales ? launch_n<64, true>(a, rows) : launch_n<64, false>(a, rows);
-  return a.k_scales ? launch_n<128, true>(a, rows) : launch_n<128, false>(a, rows);
+  return with_cfg(a.d, a.k_scales != nullptr, rows, [&](auto c) { return launch_t(a, c); });
 }
 
 }  // namespace bss

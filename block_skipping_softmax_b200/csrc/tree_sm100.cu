@@ -202,13 +202,13 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
   Plan p{};
   const long long rows = static_cast<long long>(max_q) * (Hq / Hkv);
   // Rows of a CTA.  16 sequences x 16384 keys, 8 KV heads of 128: e4m3 with 4 rows a
-  // head 98 us by 8s and 183 by 128s, with 16 rows 162 by 16s and 186 by 128s;
+  // head 98 us by 8s and 183 by 128s, with 16 rows 112 by 16s and 186 by 128s;
   // bf16 164 and 165 with 4 rows (but one sequence of 500 keys 11 and 14.4), 186 and
   // 165 with 16.
   p.per = rows <= 8 ? 8 : rows <= 16 && e4m3 ? 16 : kManyRows;
   p.planes = static_cast<int>((rows + p.per - 1) / p.per);
   const long long tiles = (L + kPage - 1) / kPage, heads = static_cast<long long>(B) * Hkv;
-  const long long slots = 148 * (p.per < kManyRows ? tree_few_ctas() : 2);
+  const long long slots = 148 * (p.per < kManyRows ? tree_few_ctas(d, e4m3, p.per) : 2);
   const long long fit = p.planes < slots ? slots / p.planes : 1;
   // A CTA for each KV head, and no merge, where its tiles are few, or where the
   // heads are more than the CTAs that run at once and rounds of them cost less
