@@ -214,10 +214,14 @@ Plan plan_of(int B, int max_q, int Hq, int Hkv, int L, int d, bool e4m3) {
   // heads are more than the CTAs that run at once and rounds of them cost less
   // than equal pieces: in tiles, rounds * (tiles + kSegment) against the equal piece
   // and its segments.  (16 x 512 e4m3 keys, 1 token: 9.4 us, 11.5 divided; 16 x 1024
-  // 13.6 and 15.2, but one sequence of 1024 13.3 and 10.5; 100 x 900 keys 43 and 49.)
+  // 13.6 and 15.2, but one sequence of 1024 13.3 and 10.5; 100 x 900 keys 43 and 50.)
+  // L is only a limit, and a sequence that alone comes near it would hold up its
+  // few CTAs, so the rounds are for short limits (222 sequences of 500 keys but one,
+  // that of 2000 keys: 67 us, 61 divided, of 4096 83 and 62, of 100000 850 and 97;
+  // 222 that all have 2000 keys 154 and 157, 4096 292 and 298).
   const long long rounds = (heads + fit - 1) / fit;
-  if (tiles <= 8 || (rounds > 1 && 2 * rounds * (tiles + kSegment) <
-                                       2 * (heads * tiles / fit) + (2 * heads / fit + 3) * kSegment)) {
+  if (tiles <= 8 || (tiles <= 32 && rounds > 1 && 2 * rounds * (tiles + kSegment) <
+                                                      2 * (heads * tiles / fit) + (2 * heads / fit + 3) * kSegment)) {
     p.min_tiles = 0;
     p.ctas = static_cast<int>(heads);
     return p;
