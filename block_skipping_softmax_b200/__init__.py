@@ -610,6 +610,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     if n_freq:
         if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous():
             raise _no(what, "inv_freq must be contiguous float32")
+        if positions is None:
+            raise _no(what, "a rotation needs positions")
         shape = positions.shape
         if (positions.dtype is not torch.int32 or (N > 1 and positions.stride(-1) != 1) or
                 not (shape == (N,) or (axes == 4 and shape == (B, N)))):
