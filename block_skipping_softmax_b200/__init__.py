@@ -812,6 +812,8 @@ def _tree(what, q, K, V, K_scales, V_scales, block_table, seq_lens, cu_q, max_q,
     B = seq_lens.numel()
     if len(table) != 2 or table[0] != B or cu_q.numel() != B + 1:
         raise _no(what, "block_table must be [B, max_pages] and cu_q [B + 1]")
+    if max_q >> 31 or max_seq_len >> 31:  # the C interface would take them for others
+        raise _no(what, "max_q and max_seq_len must be ints of 31 bits")
     tensors = [q, K, V, block_table, seq_lens, cu_q]
     if K_scales is not None:
         tensors += (K_scales, V_scales)
