@@ -21,10 +21,14 @@
 // Measured, 16 sequences x 16384 keys, 8 KV heads: e4m3 of 128 with 4 rows 98 us
 // (5.6 TB/s of the 6.55 of a copy), with 16 rows 112 (4.9 TB/s); of 64 with 4 rows
 // 58 and with 16 rows 75 (4.7 and 3.7 TB/s); bf16 of 128 166 (6.5 TB/s), of 64 90.
-// 16 x 32768 e4m3 keys, 4 rows: 187 (5.9 TB/s); 250 with the rows on the MMAs' long
-// side and one warp that only copied.  Heads of 128 with 16 rows take 231 registers
-// and 77 KB, two CTAs an SM; with three asked for, of which two fitted, the third
-// of the equal pieces came after the others, and 212 bytes were spilled (163 us).
+// 16 x 32768 e4m3 keys, 4 rows: 184 (5.9 TB/s); 250 with the rows on the MMAs' long
+// side and one warp that only copied.  Heads of 64 take three quarters of the
+// instructions of heads of 128 for half the bytes (scales, mask, softmax and sums
+// go by the key): 12 warps an SM, half of the issue slots used, stalls of fixed
+// latency.  Heads of 128 with 16 rows take 231 registers and 77 KB, two CTAs an SM
+// (8 warps, 40% of the issue slots, tensor pipe 30%); with three asked for, of which
+// two fitted, the third of the equal pieces came after the others, and 212 bytes
+// were spilled (163 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -19,19 +19,24 @@
 // conversion go on across their borders.  Rows past the last one are zero
 // queries, and softmax warps without a row only keep step.
 //
-// Measured, 16 sequences x 16384 keys, 8 KV heads, with 16 / 64 / 128 rows a head:
-//   bf16 of 128  169 / 177 / 195 us   of 64  100 / 118 / 140
-//   e4m3 of 128  186 / 202 / 231      of 64  141 (32 rows) / 163 / 194
-// bf16 is bound by HBM up to 64 rows (6.1 TB/s and more).  With 512 rows a head (64
-// tokens x 64 heads over 4 x 16384 keys: 147 us and 12 of the merge; 194 a pass under
-// a load of seconds, which the power limit slows) the tensor pipe, the ex2 unit and the issue slots are each busy for 46 to 49% of the
+// Measured, 16 sequences x 16384 keys, 8 KV heads, with 32 / 64 / 128 rows a head:
+//   bf16 of 128  171 / 176 / 196 us   of 64  100 / 116 / 141
+//   e4m3 of 128  189 / 198 / 226      of 64  137 / 161 / 190
+// bf16 of 128 is bound by HBM up to 64 rows (6.1 TB/s and more).  With 512 rows a head
+// (64 tokens x 64 heads over 4 x 16384 keys: 158 us, 12 of them the merge; 190 to 205
+// a pass under a load of seconds, which the power limit slows; heads of 64 140) the
+// tensor pipe, the ex2 unit and the issue slots are each busy for 46 to 49% of the
 // time: what counts is the latency of S, softmax and P, with two warps a scheduler
-// to hide it.  e4m3 adds the latency of the conversion, and more warps to the same
-// schedulers.  A segment's change costs 7 us: 3 for O, 3 for Q, 1 for the first S;
-// writing Q ahead of O gained nothing.  Slower: codes of K straight into 8-bit MMAs,
-// the query as two e4m3 terms (230 us against 210 then, with 64 rows); two softmax
-// warps to a row, half the keys each (bf16 219 against 206 with 128 rows, 145
-// against 123 for heads of 64 with 64).
+// to hide it.  Heads of 64 have half the bytes and MMAs behind the same chain, so it
+// shows from 64 rows on (4.7 TB/s; tensor pipe and ex2 unit 30% busy, issue slots 37%).
+// e4m3 adds the latency of the conversion, and more warps to the same schedulers, and
+// is slower than bf16 at all of these (512 rows: 226 us, of 64 191): its cache is half
+// the size, but here that is all it gains.  Its 64 registers a thread at launch cost 128
+// bytes of spills (heads of 64: 120).  A segment's change costs 7 us: 3 for O, 3 for Q,
+// 1 for the first S; writing Q ahead of O gained nothing.  Slower: codes of K straight
+// into 8-bit MMAs, the query as two e4m3 terms (230 us against 210 then, with 64 rows);
+// two softmax warps to a row, half the keys each (bf16 219 against 206 with 128 rows,
+// 145 against 123 for heads of 64 with 64).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

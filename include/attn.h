@@ -402,11 +402,11 @@ ATTN_API int attn_cache_read_e4m3(const void* K_codes, const void* V_codes, cons
  *              a sequence this is the decode of single tokens.
  *   max_q      1 to 64.
  *   A token that sees no key gets 0.  Slots past len_b may hold anything, which
- *   changes no bit of o.  What is not finite goes by the formula: a query with
- *   inf or NaN gives NaN (of scores that are all -inf too), a key reaches the
- *   tokens that see it by its score (of -inf: no weight), a value by its product
- *   with their weight, or, drafted, as NaN in all elements or in its own.  None
- *   reaches a token that does not see it.
+ *   changes no bit of o.  What is not finite goes by the formula, and reaches no
+ *   token that does not see it: a query with inf or NaN gives NaN (if all its
+ *   scores are -inf too); a key of score NaN or inf gives NaN, one of score -inf
+ *   has no weight; a value gives NaN or inf at any weight, a drafted one NaN, in
+ *   its own elements at least.
  *   Sums are held in fp32, their terms being a value times at most 2^8: results
  *   are finite and exact to that if len_b max|v| stays below 2^120, and scores if
  *   q k does.
@@ -434,8 +434,9 @@ ATTN_API int attn_tree_paged(const void* q, const void* K_pages, const void* V_p
  * attn_cache_read_e4m3 reads back, with these limits: len_b max|v| below 2^113
  * (terms of the sums carry up to 2^15) and max|k| up to 2^104 (scores are held at
  * 2^14 to 2^15 of the query's largest element); an element of q smaller than 2^-28
- * of the query's largest is off by up to 2^-40 of that one.  A key or value whose
- * scale is NaN makes the tokens that see it NaN.
+ * of the query's largest is off by up to 2^-40 of that one, and a key's weight by
+ * up to 2^-12 of itself or 2^-32 of the row's largest.  A key or value whose scale
+ * is NaN makes the tokens that see it NaN.
  */
 ATTN_API int attn_tree_paged_e4m3(const void* q, const void* K_codes, const void* V_codes,
                                   const float* K_scales, const float* V_scales,
